@@ -84,6 +84,11 @@ const char* moe355_version(void);
 /* Expert weight formats. */
 #define MOE355_W_INT4_G64   0  /* int4 affine, group 64 along the input [Edge0, section 2 "Quantization"] */
 #define MOE355_W_MXFP4      1  /* OCP MX v1.0: e2m1 elements, e8m0 scale per 32 along the input */
+#define MOE355_W_INT8       2  /* symmetric int8, one fp32 scale per output channel (int8 calls below) */
+
+/* Element types of the calls that take more than one. */
+#define MOE355_F32   0
+#define MOE355_BF16  1
 
 /*
  * One MoE layer's shape and routing (the model description the Edge0 page
@@ -110,6 +115,10 @@ typedef struct {
  * [out, in/2] (element 2c in the low nibble of byte c), s bf16 [out, in/64]
  * and b bf16 [out, in/64] (weight = s*q + b); MXFP4 stores q uint8 [out, in/2]
  * (e2m1 codes, same nibble order) and e uint8 [out, in/32] (scale 2^(e-127)).
+ * MOE355_W_INT8 stores q int8 [out, in] row by row and s fp32 [out] (weight =
+ * s*q; S = 3 H I + 4 (2 I + H)); this form is what the int8 calls read, from the
+ * pool, the slots and the layer buffer alike: it is not packed.  Every call that
+ * reads int4 or MXFP4 weights refuses it.
  * Returns 0 for an invalid descriptor.
  */
 int64_t moe355_expert_bytes(const moe355_layer_desc* d);
@@ -509,13 +518,131 @@ moe355_status moe355_prefill_layers(const moe355_layer_desc* d, int32_t n_layers
 moe355_status moe355_combine(int32_t T, int32_t H, int32_t k, const float* y,
                              const float* topk_w, float* out, hipStream_t stream);
 
+/*
+ * Routing by scores, with a balance bias.  Per token, over logits l [E]:
+ *   score   s_e = sigmoid(l_e), or softmax over the row's E logits;
+ *   choice  c_e = s_e + bias_e (bias null: 0).  The bias steers the selection (it
+ *           balances the experts' load) and enters no weight;
+ *   groups  n_group blocks of E/n_group consecutive experts, ranked by the sum of
+ *           their two largest choices; the best topk_group are kept;
+ *   ids     the k largest choices inside the kept groups, in descending order;
+ *   w_j     s of the chosen expert, divided by (the sum over the chosen + 1e-20)
+ *           when renorm is not 0, times scale.
+ * Scores, choices and sums are fp64, so decisions equal any other fp64
+ * evaluation's; ties go to the lower group and the lower id.  An expert whose
+ * logit or bias is -inf or NaN is not selectable: it adds nothing to its group's
+ * rank, comes after every selectable expert of the kept groups (by id) and has
+ * weight 0 if it is taken for want of others; a row of such logits therefore gets
+ * ids and zero weights.  A logit of +inf has the score 1 (softmax: the row's +inf
+ * logits share the mass).
+ * logits: device [T, E] of logits_type (MOE355_F32 or MOE355_BF16), rows
+ * logits_stride elements apart; bias: device fp32 [E] or null; topk_ids: device
+ * int32 [T, k]; topk_w: device fp32 [T, k].
+ * Limits: E <= 512, k <= 32, n_group <= 64 with groups of at least 2 experts,
+ * k <= topk_group * E / n_group.  Errors: MOE355_EINVAL for a bad descriptor, type
+ * or stride, null pointers or T < 0; MOE355_ENOTSUP beyond the limits.
+ */
+#define MOE355_SCORE_SOFTMAX  0
+#define MOE355_SCORE_SIGMOID  1
+typedef struct {
+    int32_t n_experts;   /* E */
+    int32_t top_k;       /* k */
+    int32_t score;       /* MOE355_SCORE_* */
+    int32_t n_group;     /* 1: no groups */
+    int32_t topk_group;
+    int32_t renorm;
+    float   scale;
+} moe355_router_desc;
+
+moe355_status moe355_route_scored(const moe355_router_desc* r, const void* logits,
+                                  int32_t logits_type, int64_t logits_stride, const float* bias,
+                                  int32_t T, int32_t* topk_ids, float* topk_w,
+                                  hipStream_t stream);
+
+/*
+ * Symmetric int8 quantisation of bf16 rows, one scale per row (per token):
+ * a = max |x|, r = 127 / a, code = rint(x r) (ties to even), scale = a / 127, each
+ * step rounded to fp32, so the codes are defined bit for bit.  A row with
+ * a < 2^-100 gets codes and scale 0; a row that holds an infinity or NaN gets
+ * codes 0 and the scale NaN, which makes every product of it NaN.
+ * x: device bf16, `rows` rows of `cols` values x_stride elements apart; codes:
+ * device int8, rows codes_stride bytes apart; scales: device fp32 [rows].
+ * Rows at 16-byte addresses with cols a multiple of 8 run on wide loads.
+ * Errors: MOE355_EINVAL for rows < 0, cols < 1, strides below cols or null pointers.
+ */
+moe355_status moe355_quantize_i8(const void* x_bf16, int64_t x_stride, int64_t rows, int32_t cols,
+                                 int8_t* codes, int64_t codes_stride, float* scales,
+                                 hipStream_t stream);
+
+/*
+ * Int8 matrix product with a scale per row of each operand (per token and per
+ * output channel): out[m, n] = a_scale[m] b_scale[n] sum_k a[m, k] b[n, k].  The
+ * sum is exact in int32; it is converted to fp32, multiplied by a_scale and then
+ * b_scale, and rounded once more if out is bf16.  Both operands are K-contiguous
+ * (b is a weight [out, in]): the dense layers beside the experts (a shared
+ * expert, projections) with codes from moe355_quantize_i8.
+ * a: device int8 [M, K], b: device int8 [N, K], out: device [M, N] of out_type
+ * (MOE355_F32 or MOE355_BF16); rows are a_stride, b_stride bytes and out_stride
+ * elements apart.  a_scale: device fp32 [M]; b_scale: device fp32 [N].
+ * M = 0 enqueues nothing.  Limits: K a multiple of 16 up to 65536; rows of codes
+ * at multiples of 16 bytes, strides below 2^23.  Errors: MOE355_EINVAL for sizes,
+ * strides or null pointers; MOE355_ENOTSUP beyond the limits.
+ */
+moe355_status moe355_matmul_i8(const int8_t* a, int64_t a_stride, const float* a_scale,
+                               const int8_t* b, int64_t b_stride, const float* b_scale, int32_t M,
+                               int32_t N, int32_t K, void* out, int32_t out_type,
+                               int64_t out_stride, hipStream_t stream);
+
+/*
+ * Expert FFN over MOE355_W_INT8 experts, both products in int8 with a scale per
+ * row of activations and per weight row:
+ *   x^ = moe355_quantize_i8(x_t);  g, u = the moe355_matmul_i8 of x^ with gate, up (fp32);
+ *   h = bf16(silu(g) u);  h^ = moe355_quantize_i8(h);  y = the product of h^ with down;
+ *   out[t] = bf16(sum_j topk_w[t, j] y[t, j]), summed in fp32, j ascending.
+ * A slot whose id lies outside [0, E) adds nothing (padding).  out: device bf16
+ * [T, H].  No atomics: the output is the same on every run.
+ *
+ * moe355_expert_ffn_prefill_i8: any T, over the buckets of moe355_permute for the
+ * same topk_ids, with the whole layer resident (layer_w: device [E * S]); y is
+ * held in bf16 before the sum.  ws: moe355_workspace_bytes(d, T,
+ * MOE355_MODE_PREFILL_I8) bytes.
+ *
+ * moe355_expert_ffn_decode_i8: T*k <= 256, y in fp32.  With exp = null the distinct
+ * experts are found from topk_ids and read from pool + (layer*E + e) * S; else
+ * uniq, counts and plan of the same ids (moe355_dedup, moe355_classify_evict,
+ * moe355_route_plan) say which experts to run, and with a cache an expert whose
+ * plan names a slot is read from it (filled by then, e.g. by moe355_cache_fill).
+ * ws: moe355_workspace_bytes(d, T, MOE355_MODE_DECODE_I8) bytes, of which
+ * nothing has to be zeroed or is kept between calls.
+ *
+ * Limits: hidden and inter multiples of 64 up to 16384, E <= 1024, prefill T*H <
+ * 2^32; x, the weights, out at multiples of 16 bytes, ws of 256.  Calls that share
+ * a workspace must not overlap.  Errors: MOE355_EINVAL for a bad descriptor (or
+ * one of another format), null or misaligned pointers; MOE355_ENOTSUP beyond the
+ * limits; MOE355_ECAPACITY for a short workspace or lists.
+ */
+moe355_status moe355_expert_ffn_prefill_i8(const moe355_layer_desc* d, const void* x_bf16,
+                                           int32_t T, const int32_t* topk_ids, const float* topk_w,
+                                           const uint8_t* layer_w, const int32_t* perm,
+                                           const int32_t* offsets, void* out_bf16, void* ws,
+                                           size_t ws_bytes, hipStream_t stream);
+
+moe355_status moe355_expert_ffn_decode_i8(const moe355_layer_desc* d, const void* x_bf16,
+                                          int32_t T, const int32_t* topk_ids, const float* topk_w,
+                                          const moe355_cache* cache, const uint8_t* pool,
+                                          int32_t layer, const moe355_classify_out* exp,
+                                          void* out_bf16, void* ws, size_t ws_bytes,
+                                          hipStream_t stream);
+
 #define MOE355_MODE_DECODE   0
 #define MOE355_MODE_PREFILL  1
 #define MOE355_MODE_PERMUTE  2
 #define MOE355_MODE_PREFILL_MX 3
+#define MOE355_MODE_DECODE_I8  4
+#define MOE355_MODE_PREFILL_I8 5
 /* Scratch bytes a call of the given mode needs for T tokens.  No page defines
  * this call; it sizes the caller-owned workspaces above.  Returns 0 for an
- * invalid descriptor, T < 0 or an unknown mode. */
+ * invalid descriptor, T < 0, an unknown mode or a mode of another weight format. */
 size_t moe355_workspace_bytes(const moe355_layer_desc* d, int32_t T, int32_t mode);
 
 #ifdef __cplusplus

@@ -11,13 +11,15 @@ import ctypes
 import os
 
 from . import abi
-from .abi import (LayerDesc, Cache, EvictPolicy, ClassifyOut, ROUTE_SOFTMAX_TOPK,
-                  ROUTE_SIGMOID_GROUP, W_INT4_G64, W_MXFP4, MODE_DECODE, MODE_PREFILL,
-                  MODE_PERMUTE, MODE_PREFILL_MX, Moe355Error, lib_path, load)
+from .abi import (LayerDesc, RouterDesc, Cache, EvictPolicy, ClassifyOut, ROUTE_SOFTMAX_TOPK,
+                  ROUTE_SIGMOID_GROUP, SCORE_SOFTMAX, SCORE_SIGMOID, W_INT4_G64, W_MXFP4, W_INT8,
+                  F32, BF16, MODE_DECODE, MODE_PREFILL, MODE_PERMUTE, MODE_PREFILL_MX, MODE_DECODE_I8,
+                  MODE_PREFILL_I8, Moe355Error, lib_path, load)
 from .ops import (router_logits, route, dedup, classify_evict, cache_fill, cache_rebuild,
                   permute, expert_ffn_decode, decode_layer, decode_layer_static, route_plan,
                   evict_fill,
                   expert_ffn_prefill, expert_ffn_prefill_mx, quantize_mx, prefill_layers, combine,
+                  route_scored, quantize_i8, matmul_i8, expert_ffn_prefill_i8, expert_ffn_decode_i8,
                   workspace_bytes, pack_experts,
                   expert_bytes, version, check_build, error_word, check_error, ERR_WAIT,
                   ERR_F16_RANGE, DeviceCache, DeviceClassifyOut)
@@ -32,5 +34,8 @@ __all__ = [
     "evict_fill",
     "expert_ffn_prefill",
     "combine", "workspace_bytes", "pack_experts", "expert_bytes", "version", "check_build",
+    "RouterDesc", "SCORE_SOFTMAX", "SCORE_SIGMOID", "W_INT8", "F32", "BF16", "MODE_DECODE_I8",
+    "MODE_PREFILL_I8", "route_scored", "quantize_i8", "matmul_i8", "expert_ffn_prefill_i8",
+    "expert_ffn_decode_i8",
     "error_word", "check_error", "ERR_WAIT", "ERR_F16_RANGE", "DeviceCache", "DeviceClassifyOut",
 ]

@@ -10,10 +10,17 @@ ROUTE_SOFTMAX_TOPK = 0
 ROUTE_SIGMOID_GROUP = 1
 W_INT4_G64 = 0
 W_MXFP4 = 1
+W_INT8 = 2
+F32 = 0
+BF16 = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 MODE_DECODE = 0
 MODE_PREFILL = 1
 MODE_PERMUTE = 2
 MODE_PREFILL_MX = 3
+MODE_DECODE_I8 = 4
+MODE_PREFILL_I8 = 5
 
 c_i32 = ctypes.c_int32
 c_i64 = ctypes.c_int64
@@ -24,6 +31,11 @@ class LayerDesc(ctypes.Structure):
     _fields_ = [("hidden", c_i32), ("inter", c_i32), ("n_experts", c_i32), ("top_k", c_i32),
                 ("route", c_i32), ("n_group", c_i32), ("topk_group", c_i32),
                 ("route_scale", ctypes.c_float), ("wfmt", c_i32)]
+
+
+class RouterDesc(ctypes.Structure):
+    _fields_ = [("n_experts", c_i32), ("top_k", c_i32), ("score", c_i32), ("n_group", c_i32),
+                ("topk_group", c_i32), ("renorm", c_i32), ("scale", ctypes.c_float)]
 
 
 class Cache(ctypes.Structure):
@@ -86,6 +98,16 @@ _SIGS = {
     "moe355_prefill_layers": (c_i32, [_P(LayerDesc), c_i32, c_i32, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr,
                                       c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, ctypes.c_size_t,
                                       c_ptr, ctypes.c_size_t, c_i32, c_ptr, c_ptr]),
+    "moe355_route_scored": (c_i32, [_P(RouterDesc), c_ptr, c_i32, c_i64, c_ptr, c_i32, c_ptr, c_ptr,
+                                    c_ptr]),
+    "moe355_quantize_i8": (c_i32, [c_ptr, c_i64, c_i64, c_i32, c_ptr, c_i64, c_ptr, c_ptr]),
+    "moe355_matmul_i8": (c_i32, [c_ptr, c_i64, c_ptr, c_ptr, c_i64, c_ptr, c_i32, c_i32, c_i32, c_ptr,
+                                 c_i32, c_i64, c_ptr]),
+    "moe355_expert_ffn_prefill_i8": (c_i32, [_P(LayerDesc), c_ptr, c_i32, c_ptr, c_ptr, c_ptr,
+                                             c_ptr, c_ptr, c_ptr, c_ptr, ctypes.c_size_t, c_ptr]),
+    "moe355_expert_ffn_decode_i8": (c_i32, [_P(LayerDesc), c_ptr, c_i32, c_ptr, c_ptr, _P(Cache),
+                                            c_ptr, c_i32, _P(ClassifyOut), c_ptr, c_ptr,
+                                            ctypes.c_size_t, c_ptr]),
     "moe355_combine": (c_i32, [c_i32, c_i32, c_i32, c_ptr, c_ptr, c_ptr, c_ptr]),
     "moe355_workspace_bytes": (ctypes.c_size_t, [_P(LayerDesc), c_i32, c_i32]),
 }

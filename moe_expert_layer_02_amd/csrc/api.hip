@@ -3,7 +3,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
-#include "internal.h"
+#include "i8.h"
 
 namespace moe355 {
 
@@ -53,7 +53,8 @@ bool expert_layout(const moe355_layer_desc* d, ExpertLayout* L) {
     return true;
 }
 
-moe355_status check_desc(const moe355_layer_desc* d) {
+// The shape of any layer, whatever its weight format.
+moe355_status check_desc_any(const moe355_layer_desc* d) {
     MOE355_REQUIRE(d, MOE355_EINVAL, "null layer descriptor");
     MOE355_REQUIRE(d->hidden > 0 && d->inter > 0 && d->n_experts > 0, MOE355_EINVAL,
                    "descriptor: H=%d I=%d E=%d", d->hidden, d->inter, d->n_experts);
@@ -61,14 +62,33 @@ moe355_status check_desc(const moe355_layer_desc* d) {
                    d->top_k);
     MOE355_REQUIRE(d->route == MOE355_ROUTE_SOFTMAX_TOPK || d->route == MOE355_ROUTE_SIGMOID_GROUP,
                    MOE355_EINVAL, "descriptor: route=%d", d->route);
-    MOE355_REQUIRE(d->wfmt == MOE355_W_INT4_G64 || d->wfmt == MOE355_W_MXFP4, MOE355_EINVAL,
-                   "descriptor: wfmt=%d", d->wfmt);
+    MOE355_REQUIRE(d->wfmt == MOE355_W_INT4_G64 || d->wfmt == MOE355_W_MXFP4 || d->wfmt == MOE355_W_INT8,
+                   MOE355_EINVAL, "descriptor: wfmt=%d", d->wfmt);
     if (d->route == MOE355_ROUTE_SIGMOID_GROUP)
         MOE355_REQUIRE(d->n_group >= 1 && d->topk_group >= 1 && d->topk_group <= d->n_group,
                        MOE355_EINVAL, "descriptor: n_group=%d topk_group=%d", d->n_group,
                        d->topk_group);
     MOE355_REQUIRE(d->hidden % 64 == 0 && d->inter % 64 == 0, MOE355_ENOTSUP,
                    "descriptor: H=%d and I=%d must be multiples of 64", d->hidden, d->inter);
+    return MOE355_OK;
+}
+
+// A layer of the 4-bit formats (every call that reads packed weights).
+moe355_status check_desc(const moe355_layer_desc* d) {
+    moe355_status st = check_desc_any(d);
+    if (st) return st;
+    MOE355_REQUIRE(d->wfmt != MOE355_W_INT8, MOE355_EINVAL, "descriptor: wfmt=%d (int8 experts have calls of their own)",
+                   d->wfmt);
+    return MOE355_OK;
+}
+
+// A layer of int8 experts within the int8 calls' limits.
+moe355_status check_desc_i8(const moe355_layer_desc* d, const char* what) {
+    moe355_status st = check_desc_any(d);
+    if (st) return st;
+    MOE355_REQUIRE(d->wfmt == MOE355_W_INT8, MOE355_EINVAL, "%s: int8 experts only (wfmt=%d)", what, d->wfmt);
+    MOE355_REQUIRE(d->hidden <= 16384 && d->inter <= 16384 && d->n_experts <= 1024, MOE355_ENOTSUP,
+                   "%s: H=%d I=%d (at most 16384), E=%d (at most 1024)", what, d->hidden, d->inter, d->n_experts);
     return MOE355_OK;
 }
 
@@ -102,17 +122,23 @@ extern "C" const char* moe355_version(void) { return "libmoe355 0.2 gfx950 src:"
 
 extern "C" int64_t moe355_expert_bytes(const moe355_layer_desc* d) {
     ExpertLayout L;
-    if (check_desc(d) != MOE355_OK || !expert_layout(d, &L)) return 0;
+    if (check_desc_any(d) != MOE355_OK) return 0;
+    if (d->wfmt == MOE355_W_INT8) return i8_layout(d).bytes;
+    if (!expert_layout(d, &L)) return 0;
     return L.bytes;
 }
 
 extern "C" size_t moe355_workspace_bytes(const moe355_layer_desc* d, int32_t T, int32_t mode) {
-    if (check_desc(d) != MOE355_OK || T < 0) return 0;
+    if (check_desc_any(d) != MOE355_OK || T < 0) return 0;
+    const bool i8_mode = mode == MOE355_MODE_DECODE_I8 || mode == MOE355_MODE_PREFILL_I8;
+    if (mode != MOE355_MODE_PERMUTE && i8_mode != (d->wfmt == MOE355_W_INT8)) return 0;
     switch (mode) {
         case MOE355_MODE_DECODE: return decode_ws_bytes(d, T);
         case MOE355_MODE_PREFILL: return prefill_ws_bytes(d, T);
         case MOE355_MODE_PERMUTE: return permute_ws_bytes(d->n_experts, T, d->top_k);
         case MOE355_MODE_PREFILL_MX: return prefill_mx_ws_bytes(d, T);
+        case MOE355_MODE_DECODE_I8: return decode_i8_ws_bytes(d, T);
+        case MOE355_MODE_PREFILL_I8: return prefill_i8_ws_bytes(d, T);
         default: return 0;
     }
 }

@@ -25,7 +25,8 @@ struct ExpertLayout {
     int64_t b_off[3] = {0, 0, 0};
 };
 bool expert_layout(const moe355_layer_desc* d, ExpertLayout* L);
-moe355_status check_desc(const moe355_layer_desc* d);
+moe355_status check_desc(const moe355_layer_desc* d);       // of the 4-bit formats
+moe355_status check_desc_any(const moe355_layer_desc* d);   // shape only, any format
 moe355_status check_cache(const moe355_cache* c);
 moe355_status check_out(const moe355_classify_out* o, bool full, int n_ids);
 

@@ -147,7 +147,7 @@ extern "C" moe355_status moe355_route_plan(const moe355_layer_desc* d, const moe
                                            int32_t layer, const float* logits, int32_t T,
                                            int32_t* topk_ids, float* topk_w,
                                            moe355_classify_out* lists, hipStream_t stream) {
-    moe355_status st = check_desc(d);
+    moe355_status st = check_desc_any(d);
     if (st) return st;
     st = check_route(d);
     if (st) return st;
@@ -171,7 +171,7 @@ extern "C" moe355_status moe355_evict_fill(const moe355_layer_desc* d, const moe
                                            const int32_t* topk_ids, int32_t T,
                                            const moe355_evict_policy* p,
                                            moe355_classify_out* lists, hipStream_t stream) {
-    moe355_status st = check_desc(d);
+    moe355_status st = check_desc_any(d);
     if (st) return st;
     MOE355_REQUIRE(T >= 1 && T * d->top_k <= 256, MOE355_ENOTSUP,
                    "evict_fill: T*k=%d outside [1, 256]", T * d->top_k);

@@ -153,7 +153,7 @@ using namespace moe355;
 extern "C" moe355_status moe355_permute(const moe355_layer_desc* d, const int32_t* topk_ids,
                                         int32_t T, int32_t* perm, int32_t* offsets, void* ws,
                                         size_t ws_bytes, hipStream_t stream) {
-    moe355_status st = check_desc(d);
+    moe355_status st = check_desc_any(d);
     if (st) return st;
     MOE355_REQUIRE(offsets && (T == 0 || (topk_ids && perm)), MOE355_EINVAL,
                    "permute: null pointer");

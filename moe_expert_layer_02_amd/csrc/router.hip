@@ -71,7 +71,7 @@ using namespace moe355;
 extern "C" moe355_status moe355_router_logits(const moe355_layer_desc* d, const void* x_bf16,
                                               const float* w_router, int32_t T, float* logits,
                                               hipStream_t stream) {
-    moe355_status st = check_desc(d);
+    moe355_status st = check_desc_any(d);
     if (st) return st;
     MOE355_REQUIRE(T >= 0, MOE355_EINVAL, "router_logits: T=%d", T);
     MOE355_REQUIRE(T == 0 || (x_bf16 && w_router && logits), MOE355_EINVAL,
@@ -84,7 +84,7 @@ extern "C" moe355_status moe355_router_logits(const moe355_layer_desc* d, const 
 
 extern "C" moe355_status moe355_route(const moe355_layer_desc* d, const float* logits, int32_t T,
                                       int32_t* topk_ids, float* topk_w, hipStream_t stream) {
-    moe355_status st = check_desc(d);
+    moe355_status st = check_desc_any(d);
     if (st) return st;
     MOE355_REQUIRE(T >= 0, MOE355_EINVAL, "route: T=%d", T);
     MOE355_REQUIRE(T == 0 || (logits && topk_ids && topk_w), MOE355_EINVAL, "route: null pointer");

@@ -10,8 +10,8 @@ import ctypes
 
 import torch
 
-from .abi import (Cache, ClassifyOut, EvictPolicy, LayerDesc, MODE_DECODE, MODE_PERMUTE,
-                  MODE_PREFILL, MODE_PREFILL_MX, Moe355Error, check, load)
+from .abi import (BF16, Cache, ClassifyOut, EvictPolicy, F32, LayerDesc, MODE_DECODE, MODE_PERMUTE,
+                  MODE_PREFILL, MODE_PREFILL_MX, Moe355Error, RouterDesc, check, load)
 
 
 def _ptr(t) -> int | None:
@@ -351,3 +351,121 @@ def combine(y, topk_w, out, stream=None):
     H = out.shape[1]
     check(load().moe355_combine(T, H, k, _ptr(y), _ptr(topk_w), _ptr(out), _stream(stream)),
           "moe355_combine")
+
+
+# ---- scored routing and the int8 operators ---------------------------------
+
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _rows(t, dtype, name, shape=None):
+    """Address and row stride (in elements) of a 2-D device tensor whose rows are contiguous."""
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be 2-D{'' if shape is None else f' of shape {shape}'}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
+def _flat(t, dtype, name, numel):
+    """Address of a contiguous device tensor of exactly numel values."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} values, got {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _run(call, stream, tensors, *args):
+    """The C call on the tensors' device: its current stream, or the given one."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (t.device != dev or not t.is_cuda):
+            raise ValueError(f"{call}: every tensor must be on one GPU (got {t.device} and {dev})")
+    fn = getattr(load(), call)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if s.device_index != dev.index:
+        raise ValueError(f"{call}: the stream belongs to GPU {s.device_index}, the tensors to {dev.index}")
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s.cuda_stream)
+    check(st, call)
+
+
+def route_scored(desc: RouterDesc, logits, bias, topk_ids, topk_w, stream=None):
+    """Routing by softmax or sigmoid scores with a balance bias (or None), groups,
+    top-k and optional renormalisation.  logits [T, E] fp32 or bf16 (rows may be
+    strided); topk_ids int32 and topk_w fp32 [T, k] are written."""
+    if logits.dtype not in _TYPES:
+        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    E, k = desc.n_experts, desc.top_k
+    T = logits.shape[0]
+    lp, ld = _rows(logits, None, "logits", (T, E))
+    _run("moe355_route_scored", stream, (logits, bias, topk_ids, topk_w), ctypes.byref(desc), lp,
+         _TYPES[logits.dtype], ld, None if bias is None else _flat(bias, torch.float32, "bias", E), T,
+         _flat(topk_ids, torch.int32, "topk_ids", T * k), _flat(topk_w, torch.float32, "topk_w", T * k))
+
+
+def quantize_i8(x_bf16, codes, scales, stream=None):
+    """Int8 codes [rows, cols] and one fp32 scale per row of bf16 x (rows may be strided)."""
+    xp, ldx = _rows(x_bf16, torch.bfloat16, "x")
+    rows, cols = x_bf16.shape
+    qp, ldq = _rows(codes, torch.int8, "codes", (rows, cols))
+    _run("moe355_quantize_i8", stream, (x_bf16, codes, scales), xp, ldx, rows, cols, qp, ldq,
+         _flat(scales, torch.float32, "scales", rows))
+
+
+def matmul_i8(a, a_scale, b, b_scale, out, stream=None):
+    """out [M, N] (fp32 or bf16) = a_scale[:, None] * b_scale * (a @ b.T) of int8 a [M, K]
+    and weights b [N, K]; rows of a, b and out may be strided."""
+    if out.dtype not in _TYPES:
+        raise TypeError(f"out must be torch.float32 or torch.bfloat16, got {out.dtype}")
+    ap, lda = _rows(a, torch.int8, "a")
+    M, K = a.shape
+    N = b.shape[0]
+    bp, ldb = _rows(b, torch.int8, "b", (N, K))
+    op, ldo = _rows(out, None, "out", (M, N))
+    _run("moe355_matmul_i8", stream, (a, a_scale, b, b_scale, out), ap, lda,
+         _flat(a_scale, torch.float32, "a_scale", M), bp, ldb, _flat(b_scale, torch.float32, "b_scale", N),
+         M, N, K, op, _TYPES[out.dtype], ldo)
+
+
+def _ffn_i8_args(desc, x, topk_ids, topk_w, out):
+    T, H, k = x.shape[0], desc.hidden, desc.top_k
+    return (T, _flat(x, torch.bfloat16, "x", T * H), _flat(topk_ids, torch.int32, "topk_ids", T * k),
+            _flat(topk_w, torch.float32, "topk_w", T * k), _flat(out, torch.bfloat16, "out", T * H))
+
+
+def expert_ffn_prefill_i8(desc, x_bf16, topk_ids, topk_w, layer_w, perm, offsets, out, ws, stream=None):
+    """Expert SwiGLU over int8 experts (W_INT8 blobs) for a prompt chunk; perm and
+    offsets come from ``permute`` of the same ids.  out: bf16 [T, H]."""
+    T, x, ids, w, o = _ffn_i8_args(desc, x_bf16, topk_ids, topk_w, out)
+    wp = _flat(layer_w, torch.uint8, "layer_w", desc.n_experts * expert_bytes(desc))
+    _run("moe355_expert_ffn_prefill_i8", stream,
+         (x_bf16, topk_ids, topk_w, layer_w, perm, offsets, out, ws), ctypes.byref(desc), x, T, ids, w, wp,
+         _flat(perm, torch.int32, "perm", T * desc.top_k),
+         _flat(offsets, torch.int32, "offsets", desc.n_experts + 1), o, _ptr(ws),
+         ws.numel() * ws.element_size())
+
+
+def expert_ffn_decode_i8(desc, x_bf16, topk_ids, topk_w, cache, pool, layer: int, experts, out, ws,
+                         stream=None):
+    """Expert SwiGLU over int8 experts for a decode call (T * k <= 256).  experts: the
+    call's lists (from dedup, classify_evict or route_plan of the same ids), or None
+    without a cache.  pool: device or pinned host memory.  out: bf16 [T, H]."""
+    T, x, ids, w, o = _ffn_i8_args(desc, x_bf16, topk_ids, topk_w, out)
+    _need(pool, torch.uint8, "pool")
+    if pool.numel() < (layer + 1) * desc.n_experts * expert_bytes(desc):
+        raise ValueError(f"pool holds fewer than {layer + 1} layers of {desc.n_experts} experts")
+    on = (x_bf16, topk_ids, topk_w, pool if pool.is_cuda else None, out, ws,
+          cache.table if cache is not None else None, experts.buf if experts is not None else None)
+    _run("moe355_expert_ffn_decode_i8", stream, on, ctypes.byref(desc), x, T, ids, w,
+         ctypes.byref(cache.struct) if cache is not None else None, _pool_ptr(pool), layer,
+         ctypes.byref(experts.struct) if experts is not None else None, o, _ptr(ws),
+         ws.numel() * ws.element_size())

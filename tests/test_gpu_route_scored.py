@@ -1,0 +1,153 @@
+"""moe355_route_scored against the 64-bit form: ids equal, weights within the half
+step of their fp32 rounding (the scores are fp64 on both sides)."""
+import numpy as np
+import pytest
+
+from gpu_common import say
+from oracle import int8 as o8
+
+pytestmark = pytest.mark.gpu
+
+W_TOL = 2.0 ** -24 * (1 + 1e-6)     # one rounding to fp32; fp64 differences are below 1e-14
+
+
+def run(logits, bias, k, score, n_group, topk_group, renorm, scale, dtype, stride=0, stream=None):
+    import torch
+    import moe_expert_layer_02_amd as m
+    T, E = logits.shape
+    t = torch.from_numpy(np.ascontiguousarray(logits, dtype=np.float32)).cuda()
+    t = t.to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    if stride:
+        wide = torch.full((T, E + stride), float("nan"), dtype=t.dtype, device="cuda")
+        wide[:, :E] = t
+        t = wide[:, :E]
+    b = None if bias is None else torch.from_numpy(np.asarray(bias, dtype=np.float32)).cuda()
+    # one guard row on each side of the outputs
+    ids = torch.full((T + 2, k), -77, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 2, k), -77.0, dtype=torch.float32, device="cuda")
+    d = m.RouterDesc(E, k, m.SCORE_SOFTMAX if score == "softmax" else m.SCORE_SIGMOID, n_group, topk_group,
+                     int(renorm), scale)
+    m.route_scored(d, t, b, ids[1:T + 1], w[1:T + 1], stream=stream)
+    torch.cuda.synchronize()
+    assert (ids[[0, -1]] == -77).all() and (w[[0, -1]] == -77).all(), "wrote outside its rows"
+    return t.float().cpu().numpy(), ids[1:T + 1].cpu().numpy(), w[1:T + 1].cpu().numpy()
+
+
+def check(logits, bias, k, score="sigmoid", n_group=1, topk_group=1, renorm=True, scale=1.0, dtype="f32",
+          stride=0):
+    seen, ids, w = run(logits, bias, k, score, n_group, topk_group, renorm, scale, dtype, stride)
+    want_ids, want_w = o8.route_scored(seen, bias, k, score, n_group, topk_group, renorm, scale)
+    assert np.array_equal(ids, want_ids), np.argwhere(ids != want_ids)[:4]
+    assert np.all(np.abs(w - want_w) <= W_TOL * np.abs(want_w) + 1e-45), np.abs(w - want_w).max()
+
+
+# T, E, k, score, n_group, topk_group, bias, renorm, scale, logits, row padding
+CASES = [
+    (1, 256, 8, "sigmoid", 8, 4, True, True, 2.5, "f32", 0),
+    (1, 2, 1, "softmax", 1, 1, False, False, 1.0, "f32", 0),
+    (5, 1, 1, "sigmoid", 1, 1, True, True, 1.0, "f32", 0),
+    (37, 256, 6, "sigmoid", 8, 4, True, True, 2.5, "bf16", 8),
+    (130, 200, 7, "softmax", 1, 1, False, False, 1.0, "bf16", 0),
+    (63, 64, 64 // 2, "softmax", 1, 1, True, True, 1.0, "f32", 1),
+    (64, 65, 9, "sigmoid", 5, 3, True, False, 1.0, "f32", 3),
+    (33, 129, 12, "softmax", 3, 2, True, True, 1.5, "bf16", 5),
+    (29, 512, 32, "sigmoid", 64, 7, True, True, 1.0, "f32", 0),
+    (21, 511, 16, "softmax", 7, 7, False, True, 1.0, "f32", 0),
+    (9, 510, 10, "sigmoid", 2, 1, True, True, 1.0, "bf16", 2),
+    (3, 24, 3, "sigmoid", 12, 2, False, True, 1.0, "f32", 0),
+    (17, 8, 8, "softmax", 4, 4, True, True, 1.0, "f32", 0),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "T%d_E%d_k%d_%s_g%d.%d_%s" % (c[:6] + (c[9],)))
+def test_against_64_bits(case):
+    T, E, k, score, g, kg, bias, renorm, scale, dtype, pad = case
+    rng = np.random.default_rng(T * 1000 + E)
+    say("route_scored", case)
+    logits = rng.normal(0, 1, (T, E))
+    b = rng.normal(0, 0.1, E).astype(np.float32) if bias else None
+    check(logits, b, k, score, g, kg, renorm, scale, dtype, pad)
+
+
+@pytest.mark.parametrize("score", ("softmax", "sigmoid"))
+@pytest.mark.parametrize("groups", ((1, 1), (4, 2)))
+def test_ties_go_to_the_lower_id(score, groups):
+    """Logits of few distinct values, and a bias that makes whole groups equal."""
+    rng = np.random.default_rng(3)
+    logits = rng.integers(-2, 3, (50, 64)).astype(np.float32)
+    logits[0] = 0
+    check(logits, None, 9, score, *groups)
+    check(logits, np.zeros(64, np.float32), 9, score, *groups, dtype="bf16")
+    check(logits, (np.arange(64) % 16 == 0).astype(np.float32), 9, score, *groups)
+
+
+@pytest.mark.parametrize("score", ("softmax", "sigmoid"))
+def test_choices_a_last_bit_apart(score):
+    """Biases that leave choices 1e-9 apart and less: decided in fp64, not in fp32."""
+    E = 128
+    l = np.zeros((4, E), dtype=np.float32)
+    l[1:] = np.random.default_rng(1).normal(0, 1e-4, (3, E))
+    b = (1e-9 * np.random.default_rng(2).permutation(E)).astype(np.float32)
+    check(l, b, 16, score)
+    check(l, b, 16, score, 8, 3)
+
+
+@pytest.mark.parametrize("score", ("softmax", "sigmoid"))
+@pytest.mark.parametrize("groups", ((1, 1), (8, 3)))
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_masked_and_infinite_logits(score, groups, dtype):
+    rng = np.random.default_rng(11)
+    E, k = 64, 6
+    l = rng.normal(0, 1, (12, E)).astype(np.float32)
+    l[0] = -np.inf                              # a row with nothing left
+    l[1, 3:] = -np.inf                          # fewer than k left
+    l[2, ::2] = -np.inf
+    l[3, 5:9] = np.nan
+    l[4] = np.nan
+    l[5, 7] = np.inf
+    l[6, [2, 40, 41]] = np.inf
+    l[7] = np.finfo(np.float32).min             # a mask of the lowest value everywhere
+    l[8, ::3] = np.finfo(np.float32).min
+    l[9] = 88.0
+    l[10] = -200.0
+    l[11, 0] = 3e38
+    check(l, None, k, score, *groups, dtype=dtype)
+    b = rng.normal(0, 0.1, E).astype(np.float32)
+    b[4] = -np.inf
+    b[9] = np.nan
+    b[17] = 1e30
+    check(l, b, k, score, *groups, dtype=dtype, renorm=False)
+    b[20] = b[50] = np.inf
+    check(l, b, k, score, *groups, dtype=dtype)
+
+
+def test_empty_batch_and_other_stream():
+    import torch
+    import moe_expert_layer_02_amd as m
+    d = m.RouterDesc(16, 2, m.SCORE_SIGMOID, 1, 1, 1, 1.0)
+    e = torch.empty((0, 16), device="cuda")
+    m.route_scored(d, e, None, torch.empty((0, 2), dtype=torch.int32, device="cuda"),
+                   torch.empty((0, 2), device="cuda"))
+    s = torch.cuda.Stream()
+    rng = np.random.default_rng(0)
+    l = rng.normal(0, 1, (40, 96))
+    seen, ids, w = run(l, None, 4, "softmax", 1, 1, True, 1.0, "f32", stream=s)
+    want, _ = o8.route_scored(seen, None, 4, "softmax", 1, 1, True, 1.0)
+    assert np.array_equal(ids, want)
+
+
+def test_binding_refuses():
+    import torch
+    import moe_expert_layer_02_amd as m
+    d = m.RouterDesc(16, 2, m.SCORE_SIGMOID, 1, 1, 1, 1.0)
+    l = torch.zeros((4, 16), device="cuda")
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    w = torch.zeros((4, 2), device="cuda")
+    for bad in ((l.half(), None, ids, w), (l, None, ids.long(), w), (l, None, ids, w.double()),
+                (l, torch.zeros(16, dtype=torch.float64, device="cuda"), ids, w)):
+        with pytest.raises(TypeError):
+            m.route_scored(d, *bad)
+    for bad in ((l[:, :8], None, ids, w), (l, None, ids[:3], w), (l, torch.zeros(15, device="cuda"), ids, w),
+                (l.t().contiguous().t(), None, ids, w), (l, None, ids.cpu(), w)):
+        with pytest.raises(ValueError):
+            m.route_scored(d, *bad)
