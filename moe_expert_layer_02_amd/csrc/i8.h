@@ -56,12 +56,16 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
-// h of one element from the two int32 sums and their scales, rounded to bf16: the
-// width the intermediate is kept in between the two products of an int8 layer
-// (half the traffic of fp32; its 2^-9 is far below the code step it meets next).
+// silu(g) u = g u / (1 + e^-g).  h is kept in bf16 between the two products of an
+// int8 layer: half the traffic of fp32, and its 2^-9 is far below the code step it
+// meets next.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+// h of one element from the two int32 sums and their scales.
 __device__ __forceinline__ uint16_t swiglu_bf16(int ga, int ua, float xs, float gs, float us) {
     const float g = static_cast<float>(ga) * xs * gs, u = static_cast<float>(ua) * xs * us;
-    return f32_to_bf16(g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u);
+    return f32_to_bf16(swiglu(g, u));
 }
 
 // One int8 expert blob: byte offsets of the codes and scales of gate, up, down.
