@@ -3,9 +3,17 @@
 // top-k, weights from the unbiased scores.
 //
 // One wavefront per token.  Lane l owns experts [l*npl, l*npl + npl), npl =
-// ceil(E / 64) <= 8.  Decisions are made in fp64, so that two choices that differ
+// ceil(E / 64) <= 8.  Decisions are those of fp64, so that two choices that differ
 // by more than a few 1e-16 rank the same here as in any other fp64 evaluation;
 // equal choices go to the lower id.
+//
+// Evaluating every score and comparing in fp64 is bound by the vector units (37 us
+// for 16384 tokens of 256 experts whose logits take 3.5 us to read).  A first pass
+// therefore ranks in fp32 and accepts its result only where no decision was close:
+// every two neighbours among the k + 1 best, and the groups on both sides of the
+// limit, are further apart than twice the fp32 error, or are equal in logit and bias
+// (an exact tie, lower id first).  About one token in a thousand fails that and is
+// decided in fp64.  Weights are fp64 in both.
 #include "internal.h"
 
 namespace moe355 {
@@ -31,12 +39,10 @@ __device__ __forceinline__ uint64_t f64_order_key(double v) {
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
+// Token t in fp64.  One wavefront; c: [E] doubles of LDS of its own.
 template <bool BF16, int NPL>
-__global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_kernel(ScoreParams p) {
-    extern __shared__ double choice_lds[];   // [SR_WAVES][E], used when groups limit the choice
-    const int lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE;
-    const int t = blockIdx.x * SR_WAVES + wv;
-    if (t >= p.T) return;   // whole wavefronts leave; there is no block barrier below
+__device__ void route_fp64(const ScoreParams& p, int t, double* c) {
+    const int lane = threadIdx.x & (WAVE - 1);
     const int E = p.E, npl = (E + WAVE - 1) / WAVE;
 
     float l[NPL];
@@ -86,7 +92,6 @@ __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_kernel(ScoreParams
     uint64_t kept = ~0ull;
     const int gsize = E / p.n_group;
     if (p.topk_group < p.n_group) {
-        double* c = choice_lds + static_cast<int64_t>(wv) * E;
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
             if (have[i]) c[lane * npl + i] = choice[i];
@@ -155,16 +160,219 @@ __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_kernel(ScoreParams
     }
 }
 
+// e^x for x <= 0 by 2^(x log2 e) on the hardware: relative error below 1.8e-7 |x| +
+// 2.4e-7 (the product's two roundings and the instruction's 1 ulp).
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// The fp32 pass: false if a decision was close.  ids and weights as route_fp64
+// leaves them.  LPG: lanes per group (0: no group limit).
+template <bool BF16, int NPL>
+__device__ __forceinline__ bool route_fp32(const ScoreParams& p, int t, bool vec, int lpg) {
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int E = p.E, e0 = lane * NPL;
+    float l[NPL];
+    const int64_t at = static_cast<int64_t>(t) * p.stride + e0;
+    if (vec) {   // rows of whole, aligned lanes: one load
+        if (e0 < E) {
+            if constexpr (BF16) {
+                uint16_t v[NPL];
+                __builtin_memcpy(v, __builtin_assume_aligned(static_cast<const uint16_t*>(p.logits) + at, 2 * NPL), 2 * NPL);
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) l[i] = bf16_to_f32(v[i]);
+            } else {
+                __builtin_memcpy(l, __builtin_assume_aligned(static_cast<const float*>(p.logits) + at, NPL >= 4 ? 16 : 4 * NPL), 4 * NPL);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (e0 + i < E)
+                l[i] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p.logits)[at + i])
+                            : static_cast<const float*>(p.logits)[at + i];
+    }
+    float b[NPL];
+    bool plain = true;   // every logit of the row is finite and its bias moderate
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        b[i] = 0.0f;
+        if (e0 + i < E) {
+            if (p.bias) b[i] = p.bias[e0 + i];
+            plain = plain && __builtin_fabsf(l[i]) < 1e30f && __builtin_fabsf(b[i]) < 64.0f;
+        } else {
+            l[i] = -3.0e38f;
+        }
+    }
+    if (__ballot(!plain)) return false;
+
+    // Scores, and a bound es of their error.  Sigmoid: s (1 - s) times the relative error of
+    // e^-l, where s (1 - s) |l| <= 0.23, and the sum's and reciprocal's roundings: below 5e-7.
+    // Softmax, d below the maximum, r = 1 / sum: r e^-d (1.8e-7 d + 2.4e-7 + 8e-7 for the
+    // sum), largest at d = 0: below 1.5e-6 r.
+    float s[NPL], mx = l[0], es = 5e-7f, total = 1.0f;
+    const bool soft = p.score == MOE355_SCORE_SOFTMAX;
+    if (soft) {
+#pragma unroll
+        for (int i = 1; i < NPL; ++i) mx = fmaxf(mx, l[i]);
+        // order-preserving keys of finite floats: the integer maximum
+        mx = __uint_as_float([&] {
+            const uint32_t k = wave_max_u32(f32_order_key(mx));
+            return (k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k;
+        }());
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            s[i] = exp_fast(l[i] - mx);
+            sum += s[i];
+        }
+        total = wave_sum_dpp_f32(sum);
+        const float r = 1.0f / total;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s[i] *= r;
+        es = 1.5e-6f * r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[i]));
+    }
+    uint32_t key[NPL];   // of the choices; 0: no expert, or one of a group left out
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) key[i] = e0 + i < E ? f32_order_key(s[i] + b[i]) : 0u;
+    auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); };
+
+    if (lpg) {
+        // the two best keys of the group, by exchanges inside its lanes
+        uint32_t a1 = key[0], a2 = 0u;
+#pragma unroll
+        for (int i = 1; i < NPL; ++i) {
+            a2 = max(a2, min(a1, key[i]));
+            a1 = max(a1, key[i]);
+        }
+        for (int m = 1; m < lpg; m <<= 1) {
+            const uint32_t o1 = __shfl_xor(a1, m, WAVE), o2 = __shfl_xor(a2, m, WAVE);
+            a2 = max(min(a1, o1), max(a2, o2));
+            a1 = max(a1, o1);
+        }
+        const float g = value(a1) + value(a2);
+        const int mine = lane / lpg;
+        int rank = 0;
+        float lowest_in = 3.0e38f, highest_out = -3.0e38f;
+        for (int q = 0; q < p.n_group; ++q) {
+            const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), q * lpg));
+            if (o > g || (o == g && q < mine)) ++rank;
+        }
+        const bool kept = mine < p.n_group && rank < p.topk_group;
+        for (int q = 0; q < p.n_group; ++q) {
+            const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), q * lpg));
+            if (__builtin_amdgcn_readlane(kept ? 1 : 0, q * lpg)) lowest_in = fminf(lowest_in, o);
+            else highest_out = fmaxf(highest_out, o);
+        }
+        // four scores' errors, and the roundings of sums with biases below 64
+        if (!(lowest_in - highest_out > 4.0f * es + (p.bias ? 1.6e-5f : 5e-7f))) return false;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) key[i] = kept ? key[i] : 0u;
+    }
+
+    int my_e = 0;
+    float my_l = 0.0f, last_c = 0.0f, last_l = 0.0f, last_b = 0.0f;
+    for (int r = 0; r <= p.k; ++r) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int i = 1; i < NPL; ++i) m = max(m, key[i]);
+        const uint32_t top = wave_max_u32(m);
+        if (top == 0u) break;   // fewer than k + 1 candidates (never fewer than k)
+        const uint64_t who = __ballot(m == top);
+        const int owner = __ffsll(static_cast<unsigned long long>(who)) - 1;   // the lowest lane has the lowest ids
+        int at_i = NPL - 1;
+        float li = l[NPL - 1], bi = b[NPL - 1];
+#pragma unroll
+        for (int i = NPL - 2; i >= 0; --i)
+            if (key[i] == top) {
+                at_i = i;
+                li = l[i];
+                bi = b[i];
+            }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) key[i] = lane == owner && i == at_i ? 0u : key[i];
+        const float lo = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(li), owner));
+        const float bo = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bi), owner));
+        const int e = __builtin_amdgcn_readlane(e0 + at_i, owner);
+        const float c = value(top);
+        // two scores' errors, and the roundings of the two sums with a bias
+        const float near = 2.0f * es + 2.4e-7f * fmaxf(__builtin_fabsf(last_c), __builtin_fabsf(c));
+        if (r > 0 && !(last_c - c > near) && !(lo == last_l && bo == last_b)) return false;
+        last_c = c;
+        last_l = lo;
+        last_b = bo;
+        if (lane == r) {
+            my_e = e;
+            my_l = lo;
+        }
+    }
+
+    // weights in fp64
+    double sc;
+    if (soft) {
+        sc = exp(static_cast<double>(my_l) - static_cast<double>(mx));
+        if (p.renorm) {
+            // the row's sum cancels but for the 1e-20 beside it, where fp32 does as long as the
+            // chosen hold some mass
+            const float mass = wave_sum_dpp_f32(lane < p.k ? static_cast<float>(sc) : 0.0f);
+            if (!(mass > 1e-6f)) return false;
+            sc /= static_cast<double>(total);
+        } else {
+            double z = 0.0;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (e0 + i < E) z += exp(static_cast<double>(l[i]) - static_cast<double>(mx));
+#pragma unroll
+            for (int m = 32; m >= 1; m >>= 1) z += __shfl_xor(z, m, WAVE);
+            sc /= z;
+        }
+    } else {
+        sc = 1.0 / (1.0 + exp(-static_cast<double>(my_l)));
+    }
+    if (lane >= p.k) sc = 0.0;
+    if (p.renorm) {
+        double sum = sc;   // the first 32 lanes hold the chosen
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor(sum, m, WAVE);
+        sc = sc / (sum + 1e-20);
+    }
+    if (lane < p.k) {
+        p.ids[static_cast<int64_t>(t) * p.k + lane] = my_e;
+        p.w[static_cast<int64_t>(t) * p.k + lane] = static_cast<float>(sc * static_cast<double>(p.scale));
+    }
+    return true;
+}
+
+template <bool BF16, int NPL>
+__global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_kernel(ScoreParams p, bool fast, bool vec, int lpg) {
+    extern __shared__ double choice_lds[];   // [SR_WAVES][E], used when groups limit the choice
+    const int wv = threadIdx.x / WAVE;
+    const int t = blockIdx.x * SR_WAVES + wv;
+    if (t >= p.T) return;   // whole wavefronts leave; there is no block barrier
+    if (fast && route_fp32<BF16, NPL>(p, t, vec, lpg)) return;
+    route_fp64<BF16, NPL>(p, t, choice_lds + static_cast<int64_t>(wv) * p.E);
+}
+
 template <bool BF16>
 void launch_score_route(const ScoreParams& p, hipStream_t stream) {
     const unsigned blocks = (static_cast<unsigned>(p.T) + SR_WAVES - 1) / SR_WAVES;
-    const size_t lds = p.topk_group < p.n_group ? SR_WAVES * static_cast<size_t>(p.E) * sizeof(double) : 0;
+    const bool limit = p.topk_group < p.n_group;
+    const size_t lds = limit ? SR_WAVES * static_cast<size_t>(p.E) * sizeof(double) : 0;
     const int npl = (p.E + WAVE - 1) / WAVE;
-    auto k = npl <= 1 ? score_route_kernel<BF16, 1>
-             : npl <= 2 ? score_route_kernel<BF16, 2>
-             : npl <= 4 ? score_route_kernel<BF16, 4>
+    const int NPL = npl <= 1 ? 1 : npl <= 2 ? 2 : npl <= 4 ? 4 : SR_MAX_NPL;
+    // the fp32 pass gives lane l experts [l NPL, l NPL + NPL); a group limit has to fall
+    // on whole lanes, a power of two of them
+    const int gsize = p.E / p.n_group, lpg = limit ? gsize / NPL : 0;
+    const bool fast = !limit || (gsize % NPL == 0 && (lpg & (lpg - 1)) == 0);
+    const int width = BF16 ? 2 * NPL : NPL >= 4 ? 16 : 4 * NPL;   // alignment of a lane's load
+    const bool vec = p.E % NPL == 0 && p.stride * (BF16 ? 2 : 4) % width == 0 &&
+                     reinterpret_cast<uintptr_t>(p.logits) % width == 0;
+    auto k = NPL == 1 ? score_route_kernel<BF16, 1>
+             : NPL == 2 ? score_route_kernel<BF16, 2>
+             : NPL == 4 ? score_route_kernel<BF16, 4>
                         : score_route_kernel<BF16, SR_MAX_NPL>;
-    k<<<blocks, SR_WAVES * WAVE, lds, stream>>>(p);
+    k<<<blocks, SR_WAVES * WAVE, lds, stream>>>(p, fast, vec, lpg);
 }
 
 }  // namespace
