@@ -5,16 +5,21 @@
 // v_mfma_i32_16x16x64_i8 with the weights as the first operand (16 rows x 64
 // inputs) and up to 16 pairs of the expert as the second, so one pass over an
 // expert's bytes serves its pairs; bound by the weight bytes of the distinct
-// experts.  Four launches: quantise x, gate/up (h in bf16 by pair), quantise h,
-// down with the combine.  A down block owns 16 output rows of every token: the
-// pairs' results meet in LDS and are summed j ascending, so no atomics and a
-// deterministic output.
+// experts, and by the chain of launches and loads where those are few.
+//
+// Two kernels: gate/up (h in bf16 by pair) and down with the combine.  A down block
+// owns 16 output rows of every token: the pairs' results meet in LDS and are summed
+// j ascending, so no atomics and a deterministic output.  A small call quantises x
+// and h inside them, every block for itself (the rows are read from the L2 while
+// the weights are on their way); otherwise each has a launch of its own before it,
+// since a block would spend longer on all rows than the launch takes.
 #include "i8.h"
 
 namespace moe355 {
 namespace {
 
 constexpr int MAX_PAIRS = 256;
+constexpr int MAX_EXPERTS_I8 = 1024;
 constexpr int DN_WAVES = 8;
 
 struct DecodeI8 {
@@ -36,7 +41,14 @@ struct DecodeI8 {
     const int8_t* hq;
     const float* hs;
     uint16_t* out;
+    const uint16_t* x;
+    int lds_rows;               // bytes of one quantised row in LDS (0: rows are quantised already)
 };
+
+// A small call: rows quantised by every block.  Gate/up: one row per wavefront of its
+// four; down: at most this many values of h.
+constexpr int INLINE_TOKENS = 4, INLINE_H = 8192, INLINE_VALUES = 16384;
+constexpr int EARLY_PAIRS = 16;
 
 // Where an expert's bytes are: its cache slot, or the pool.
 __device__ __forceinline__ const uint8_t* blob_of(const DecodeI8& p, int e, int slot) {
@@ -58,21 +70,33 @@ __device__ __forceinline__ int pairs_of(const int32_t* ids, int e, int lane, int
     return n;
 }
 
-// One 16-row tile against one group of 16 columns over inputs [k0, k1) in steps
-// of 64, `step` apart.  w: this lane's row and 16-byte chunk; x: this lane's
-// column and chunk.
-__device__ __forceinline__ i32x4 dot_tile(const uint8_t* w, const int8_t* x, int k0, int k1, int step, i32x4 acc) {
-#pragma unroll 8
-    for (int k = k0; k < k1; k += step)
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4*>(w + k),
-                                                    *reinterpret_cast<const i32x4*>(x + k), acc, 0, 0, 0);
-    return acc;
-}
+// N steps of 64 inputs of one operand's tile, requested at once: from k0 on, `step`
+// apart.  p: this lane's row (or column) and 16-byte chunk.
+template <int N>
+struct Steps {
+    i32x4 v[N];
+    __device__ __forceinline__ void load(const void* p, int k0, int n, int step) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = k0 + i * step < n ? *reinterpret_cast<const i32x4*>(static_cast<const uint8_t*>(p) + k0 + i * step) : i32x4{};
+    }
+    // the products with the other operand (zero past the end on both sides)
+    __device__ __forceinline__ i32x4 dot(const Steps& x, i32x4 acc) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[i], x.v[i], acc, 0, 0, 0);
+        return acc;
+    }
+};
 
+// N: steps of gate and of up that a wavefront has in flight.  A small call has few
+// blocks and takes 8; where blocks queue, 4 leave room for twice the blocks per CU.
+template <int N>
 __global__ void __launch_bounds__(256) gate_up_i8_kernel(DecodeI8 p) {
+    extern __shared__ __attribute__((aligned(16))) int8_t rows[];   // small call: the tokens' codes
     __shared__ int32_t ids[MAX_PAIRS];
     __shared__ int32_t list[MAX_PAIRS];
     __shared__ int32_t count;
+    __shared__ float row_scales[INLINE_TOKENS];
     __shared__ i32x4 part[4][2][WAVE];
     const int tid = threadIdx.x, lane = tid & (WAVE - 1);
     const int wv = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -87,26 +111,55 @@ __global__ void __launch_bounds__(256) gate_up_i8_kernel(DecodeI8 p) {
     }
     if (e < 0 || e >= p.E) return;
     ids[tid] = tid < p.pairs ? p.ids[tid] : -1;
-    __syncthreads();
-    if (wv == 0) {
-        const int n = pairs_of(ids, e, lane, list);
-        if (lane == 0) count = n;
+    // In a call of few pairs the weights are requested before anything else is known
+    // about the expert's pairs; in a larger one many pairs share an expert, and the first
+    // of them has to be found before (loading first read 1.2 times the bytes at 96 pairs).
+    const bool early = p.uniq || p.pairs <= EARLY_PAIRS;
+    auto find_pairs = [&]() {
+        __syncthreads();
+        if (wv == 0) {
+            const int n = pairs_of(ids, e, lane, list);
+            if (lane == 0) count = n;
+        }
+    };
+    if (!early) {
+        find_pairs();
+        __syncthreads();
+        if (list[0] != u) return;
+    }
+    const uint8_t* blob = blob_of(p, e, slot);
+    const int row = lane & 15, quad = lane >> 4;
+    const uint8_t* wg = blob + p.q_off[0] + static_cast<int64_t>(f0 + row) * p.H + quad * 16;
+    const uint8_t* wu = blob + p.q_off[1] + static_cast<int64_t>(f0 + row) * p.H + quad * 16;
+    Steps<N> g0, u0;
+    g0.load(wg, wv * 64, p.H, 256);
+    u0.load(wu, wv * 64, p.H, 256);
+    const float gs = reinterpret_cast<const float*>(blob + p.s_off[0])[f0 + (tid & 15)];
+    const float us = reinterpret_cast<const float*>(blob + p.s_off[1])[f0 + (tid & 15)];
+    if (early) find_pairs();
+    if (p.lds_rows && wv < p.T) {
+        const float s = quant_row(p.x + static_cast<int64_t>(wv) * p.H, p.H, rows + wv * p.lds_rows, lane);
+        if (lane == 0) row_scales[wv] = s;
     }
     __syncthreads();
     // without lists the first pair of an expert does it
     if (count == 0 || (!p.uniq && list[0] != u)) return;
     const int n = count;
-    const uint8_t* blob = blob_of(p, e, slot);
-    const int row = lane & 15, quad = lane >> 4;
-    const uint8_t* wg = blob + p.q_off[0] + static_cast<int64_t>(f0 + row) * p.H + quad * 16;
-    const uint8_t* wu = blob + p.q_off[1] + static_cast<int64_t>(f0 + row) * p.H + quad * 16;
-    const float* gs = reinterpret_cast<const float*>(blob + p.s_off[0]) + f0;
-    const float* us = reinterpret_cast<const float*>(blob + p.s_off[1]) + f0;
     for (int g = 0; g < n; g += 16) {
         const int tok = list[min(g + row, n - 1)] / p.k;
-        const int8_t* x = p.xq + static_cast<int64_t>(tok) * p.H + quad * 16;
-        part[wv][0][lane] = dot_tile(wg, x, wv * 64, p.H, 256, i32x4{});
-        part[wv][1][lane] = dot_tile(wu, x, wv * 64, p.H, 256, i32x4{});
+        const int8_t* x = (p.lds_rows ? rows + tok * p.lds_rows : p.xq + static_cast<int64_t>(tok) * p.H) + quad * 16;
+        Steps<N> a, b, xs;
+        xs.load(x, wv * 64, p.H, 256);
+        i32x4 ga = g0.dot(xs, i32x4{}), ua = u0.dot(xs, i32x4{});
+        for (int k = wv * 64 + N * 256; k < p.H; k += N * 256) {
+            xs.load(x, k, p.H, 256);
+            a.load(wg, k, p.H, 256);
+            b.load(wu, k, p.H, 256);
+            ga = a.dot(xs, ga);
+            ua = b.dot(xs, ua);
+        }
+        part[wv][0][lane] = ga;
+        part[wv][1][lane] = ua;
         __syncthreads();
         // element i of lane l: row 4 (l / 16) + i, column l % 16
         const int f = tid & 15, c = tid >> 4;
@@ -118,59 +171,121 @@ __global__ void __launch_bounds__(256) gate_up_i8_kernel(DecodeI8 p) {
                 a += reinterpret_cast<const int*>(&part[w][0][at])[i];
                 b += reinterpret_cast<const int*>(&part[w][1][at])[i];
             }
-            const int pair = list[g + c];
-            p.h[static_cast<int64_t>(pair) * p.I + f0 + f] = swiglu_bf16(a, b, p.xs[pair / p.k], gs[f], us[f]);
+            const int pair = list[g + c], t = pair / p.k;
+            p.h[static_cast<int64_t>(pair) * p.I + f0 + f] = swiglu_bf16(a, b, p.lds_rows ? row_scales[t] : p.xs[t], gs, us);
         }
         __syncthreads();
     }
 }
 
 __global__ void __launch_bounds__(DN_WAVES* WAVE) down_i8_kernel(DecodeI8 p) {
+    extern __shared__ __attribute__((aligned(16))) int8_t rows[];   // small call: the pairs' codes
     __shared__ int32_t ids[MAX_PAIRS];
     __shared__ int32_t item[MAX_PAIRS];
+    __shared__ int32_t first[MAX_EXPERTS_I8];   // the first pair of every expert named
     __shared__ int32_t n_items;
     __shared__ int32_t lists[DN_WAVES][MAX_PAIRS];
+    __shared__ float hscale[MAX_PAIRS];
     __shared__ float y[MAX_PAIRS][16];
     const int tid = threadIdx.x, lane = tid & (WAVE - 1);
     const int wv = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const int r0 = blockIdx.x * 16;
+    int my_id = -1;
     if (tid < MAX_PAIRS) {
-        const int id = tid < p.pairs ? p.ids[tid] : -1;
-        ids[tid] = id >= 0 && id < p.E ? id : -1;
+        my_id = tid < p.pairs ? p.ids[tid] : -1;
+        if (my_id >= p.E || my_id < 0) my_id = -1;
+        ids[tid] = my_id;
+        if (my_id >= 0) first[my_id] = MAX_PAIRS;
     }
     __syncthreads();
-    if (!p.uniq && wv == 0) {   // the first pair of every expert, in order
-        int n = 0;
-        for (int g = 0; g < p.pairs; g += WAVE) {
-            const int q = g + lane, id = ids[q];
-            bool first = id >= 0;
-            for (int j = 0; j < q && first; ++j) first = ids[j] != id;
-            const uint64_t m = __ballot(first);
-            if (first) item[n + __popcll(m & ((1ull << lane) - 1))] = id;
-            n += __popcll(m);
+    if (!p.uniq) {
+        if (my_id >= 0) atomicMin(&first[my_id], tid);
+        __syncthreads();
+        if (wv == 0) {   // the experts in the order of their first pairs
+            int n = 0;
+#pragma unroll
+            for (int g = 0; g < MAX_PAIRS; g += WAVE) {
+                const int id = ids[g + lane];
+                const bool is = id >= 0 && first[id] == g + lane;
+                const uint64_t m = __ballot(is);
+                if (is) item[n + __popcll(m & ((1ull << lane) - 1))] = id;
+                n += __popcll(m);
+            }
+            if (lane == 0) n_items = n;
         }
-        if (lane == 0) n_items = n;
+        __syncthreads();
     }
-    __syncthreads();
     const int items = p.uniq ? min(p.counts[0], p.capacity) : n_items;
     const int row = lane & 15, quad = lane >> 4;
-    for (int u = wv; u < items; u += DN_WAVES) {
-        const int e = p.uniq ? p.uniq[u] : item[u];
-        if (e < 0 || e >= p.E) continue;
-        const uint8_t* blob = blob_of(p, e, p.uniq ? p.plan[u].x : -1);
-        const int n = pairs_of(ids, e, lane, lists[wv]);
-        __builtin_amdgcn_wave_barrier();
-        const uint8_t* w = blob + p.q_off[2] + static_cast<int64_t>(r0 + row) * p.I + quad * 16;
-        const float4 ds = *reinterpret_cast<const float4*>(blob + p.s_off[2] + (r0 + quad * 4) * 4);
-        for (int g = 0; g < n; g += 16) {
-            const int pair = lists[wv][min(g + row, n - 1)];
-            const i32x4 acc = dot_tile(w, p.hq + static_cast<int64_t>(pair) * p.I + quad * 16, 0, p.I, 64, i32x4{});
-            const float s = p.hs[pair];
-            if (g + row < n)
-                *reinterpret_cast<float4*>(&y[pair][quad * 4]) =
-                    make_float4(static_cast<float>(acc[0]) * s * ds.x, static_cast<float>(acc[1]) * s * ds.y,
-                                static_cast<float>(acc[2]) * s * ds.z, static_cast<float>(acc[3]) * s * ds.w);
+    auto blob_of_item = [&](int u) {   // null: none
+        const int e = u < items ? (p.uniq ? p.uniq[u] : item[u]) : -1;
+        if (e < 0 || e >= p.E) return static_cast<const uint8_t*>(nullptr);
+        return blob_of(p, e, p.uniq ? p.plan[u].x : -1);
+    };
+    auto tile_of = [&](const uint8_t* blob) {   // this lane's row and chunk
+        return blob + p.q_off[2] + static_cast<int64_t>(r0 + row) * p.I + quad * 16;
+    };
+    // A wavefront's items are one stream of chunks of 8 steps; the next chunk (of this
+    // item or the first of the next) is requested before this one's products.
+    const uint8_t *blob = blob_of_item(wv), *w = blob ? tile_of(blob) : nullptr;
+    constexpr int CHUNK = 8;
+    Steps<CHUNK> cur;
+    if (w) cur.load(w, 0, p.I, 64);
+    if (p.lds_rows) {
+        for (int q = wv; q < p.pairs; q += DN_WAVES) {
+            if (ids[q] < 0) continue;
+            const float s = quant_row(p.h + static_cast<int64_t>(q) * p.I, p.I, rows + q * p.lds_rows, lane);
+            if (lane == 0) hscale[q] = s;
         }
+        __syncthreads();
+    }
+    for (int u = wv; u < items; u += DN_WAVES) {
+        const uint8_t *next_blob = blob_of_item(u + DN_WAVES), *next_w = next_blob ? tile_of(next_blob) : nullptr;
+        if (w) {
+            const int e = p.uniq ? p.uniq[u] : item[u];
+            const int n = pairs_of(ids, e, lane, lists[wv]);
+            __builtin_amdgcn_wave_barrier();
+            const float4 ds = *reinterpret_cast<const float4*>(blob + p.s_off[2] + (r0 + quad * 4) * 4);
+            auto x_of = [&](int pair) {
+                return (p.lds_rows ? rows + pair * p.lds_rows : p.hq + static_cast<int64_t>(pair) * p.I) + quad * 16;
+            };
+            auto put = [&](int g, int pair, i32x4 acc) {
+                const float s = p.lds_rows ? hscale[pair] : p.hs[pair];
+                if (g + row < n)
+                    *reinterpret_cast<float4*>(&y[pair][quad * 4]) =
+                        make_float4(static_cast<float>(acc[0]) * s * ds.x, static_cast<float>(acc[1]) * s * ds.y,
+                                    static_cast<float>(acc[2]) * s * ds.z, static_cast<float>(acc[3]) * s * ds.w);
+            };
+            const int pair0 = n ? lists[wv][min(row, n - 1)] : 0;   // n = 0: lists of other ids; nothing is kept
+            i32x4 acc = {};
+            for (int k = 0; k < p.I; k += CHUNK * 64) {
+                // loads complete in order: the columns first, or they would wait for the weights
+                Steps<CHUNK> next, x;
+                x.load(x_of(pair0), k, p.I, 64);
+                __builtin_amdgcn_sched_barrier(0);
+                if (k + CHUNK * 64 < p.I) next.load(w, k + CHUNK * 64, p.I, 64);
+                else if (next_w) next.load(next_w, 0, p.I, 64);
+                __builtin_amdgcn_sched_barrier(0);
+                acc = cur.dot(x, acc);
+                cur = next;
+            }
+            if (n) put(0, pair0, acc);
+            for (int g = 16; g < n; g += 16) {   // more than 16 pairs: the tile again, from the caches
+                const int pair = lists[wv][min(g + row, n - 1)];
+                i32x4 more = {};
+                for (int k = 0; k < p.I; k += CHUNK * 64) {
+                    Steps<CHUNK> a, x;
+                    x.load(x_of(pair), k, p.I, 64);
+                    a.load(w, k, p.I, 64);
+                    more = a.dot(x, more);
+                }
+                put(g, pair, more);
+            }
+        } else if (next_w) {
+            cur.load(next_w, 0, p.I, 64);
+        }
+        w = next_w;
+        blob = next_blob;
     }
     __syncthreads();
     for (int i = tid; i < p.T * 16; i += DN_WAVES * WAVE) {
@@ -290,14 +405,26 @@ extern "C" moe355_status moe355_expert_ffn_decode_i8(const moe355_layer_desc* d,
     p.hq = hq;
     p.hs = hs;
     p.out = static_cast<uint16_t*>(out_bf16);
-    st = launch_quant_rows(x_bf16, p.H, T, p.H, xq, p.H, xs, stream, "expert_ffn_decode_i8 quantise x");
-    if (st) return st;
+    p.x = static_cast<const uint16_t*>(x_bf16);
+    // rows in LDS lie 16 bytes further apart than their length, so that columns fall in
+    // different banks
+    const bool inline_x = T <= INLINE_TOKENS && p.H <= INLINE_H;
+    if (!inline_x) {
+        st = launch_quant_rows(x_bf16, p.H, T, p.H, xq, p.H, xs, stream, "expert_ffn_decode_i8 quantise x");
+        if (st) return st;
+    }
     const int items = exp ? (pairs < p.E ? pairs : p.E) : pairs;
-    gate_up_i8_kernel<<<dim3(p.I / 16, items), 256, 0, stream>>>(p);
+    p.lds_rows = inline_x ? p.H + 16 : 0;
+    auto gate_up = pairs <= EARLY_PAIRS ? gate_up_i8_kernel<8> : gate_up_i8_kernel<4>;
+    gate_up<<<dim3(p.I / 16, items), 256, static_cast<size_t>(p.lds_rows) * T, stream>>>(p);
     st = check_launch("expert_ffn_decode_i8 gate_up");
     if (st) return st;
-    st = launch_quant_rows(p.h, p.I, pairs, p.I, hq, p.I, hs, stream, "expert_ffn_decode_i8 quantise h");
-    if (st) return st;
-    down_i8_kernel<<<p.H / 16, DN_WAVES * WAVE, 0, stream>>>(p);
+    const bool inline_h = pairs * p.I <= INLINE_VALUES;
+    if (!inline_h) {
+        st = launch_quant_rows(p.h, p.I, pairs, p.I, hq, p.I, hs, stream, "expert_ffn_decode_i8 quantise h");
+        if (st) return st;
+    }
+    p.lds_rows = inline_h ? p.I + 16 : 0;
+    down_i8_kernel<<<p.H / 16, DN_WAVES * WAVE, static_cast<size_t>(p.lds_rows) * pairs, stream>>>(p);
     return check_launch("expert_ffn_decode_i8 down");
 }

@@ -51,6 +51,32 @@ __device__ __forceinline__ uint2 quant8(uint4 v, float r) {
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
+// One row of n bf16 values (16-byte aligned, n a multiple of 8) to codes by one
+// wavefront; the row's scale on every lane.
+__device__ __forceinline__ float quant_row(const uint16_t* x, int n, int8_t* q, int lane) {
+    constexpr int HELD = 4;   // vectors a lane keeps between the two passes (2048 columns); the others are read again
+    uint4 v[HELD];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const int c = (i * WAVE + lane) * 8;
+        v[i] = c < n ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+    }
+    for (int c = (HELD * WAVE + lane) * 8; c < n; c += WAVE * 8)
+        top = max(top, bf16x8_top(*reinterpret_cast<const uint4*>(x + c)));
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) top = max(top, bf16x8_top(v[i]));
+    const RowScale rs = row_scale(wave_max_u32(top));
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const int c = (i * WAVE + lane) * 8;
+        if (c < n) *reinterpret_cast<uint2*>(q + c) = quant8(v[i], rs.r);
+    }
+    for (int c = (HELD * WAVE + lane) * 8; c < n; c += WAVE * 8)
+        *reinterpret_cast<uint2*>(q + c) = quant8(*reinterpret_cast<const uint4*>(x + c), rs.r);
+    return rs.scale;
+}
+
 // fp32 to bf16 bits, to nearest (ties to even); NaN stays NaN.
 __device__ __forceinline__ uint16_t f32_to_bf16(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
