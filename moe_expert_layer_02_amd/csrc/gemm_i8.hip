@@ -415,6 +415,67 @@ __global__ void __launch_bounds__(256) rows_i8_kernel(const int32_t* __restrict_
     yrow[i] = ok ? pair : pairs;
 }
 
+// Dense product of few rows: bound by reading the weights once and by latency, not by
+// the matrix cores.  A block owns 16 weight rows and up to 16 NT rows of A; its eight
+// wavefronts split K (v_mfma_i32_16x16x64_i8, the weights as the first operand) and
+// meet in LDS.
+constexpr int FEW_WAVES = 8;
+constexpr int64_t FEW_OUTPUTS = 1 << 20;
+template <int NT>
+__global__ void __launch_bounds__(FEW_WAVES* WAVE) few_rows_i8_kernel(GemmParams p) {
+    __shared__ i32x4 part[FEW_WAVES][NT][WAVE];
+    const int tid = threadIdx.x, lane = tid & (WAVE - 1);
+    const int wv = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int row = lane & 15, quad = lane >> 4;
+    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * NT;
+    const int8_t* w = p.b + static_cast<int64_t>(min(n0 + row, p.N - 1)) * p.ldb + quad * 16;
+    const int8_t* x[NT];
+    i32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        x[t] = p.a + static_cast<int64_t>(min(m0 + 16 * t + row, p.M - 1)) * p.lda + quad * 16;
+        acc[t] = i32x4{};
+    }
+    // steps of 64 inputs, FEW_WAVES apart; AHEAD of them requested at once.  A lane whose
+    // 16 inputs lie past K takes zeros.
+    constexpr int AHEAD = NT >= 4 ? 4 : 8;
+    for (int k0 = wv * 64; k0 < p.K; k0 += AHEAD * FEW_WAVES * 64) {
+        i32x4 b[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int k = k0 + i * FEW_WAVES * 64;
+            b[i] = k + quad * 16 < p.K ? *reinterpret_cast<const i32x4*>(w + k) : i32x4{};
+        }
+        i32x4 a[AHEAD][NT];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int k = k0 + i * FEW_WAVES * 64;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) a[i][t] = k + quad * 16 < p.K ? *reinterpret_cast<const i32x4*>(x[t] + k) : i32x4{};
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[i], a[i][t], acc[t], 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) part[wv][t][lane] = acc[t];
+    __syncthreads();
+    // element i of lane l: weight row 4 (l / 16) + i, row of A l % 16
+    for (int o = tid; o < NT * 256; o += FEW_WAVES * WAVE) {
+        const int n = o & 15, m = (o >> 4) & 15, t = o >> 8;
+        if (n0 + n >= p.N || m0 + 16 * t + m >= p.M) continue;
+        int sum = 0;
+#pragma unroll
+        for (int q = 0; q < FEW_WAVES; ++q) sum += reinterpret_cast<const int*>(&part[q][t][(n >> 2) * 16 + m])[n & 3];
+        const int r = m0 + 16 * t + m;
+        const float v = static_cast<float>(sum) * p.as[r] * p.bs[n0 + n];
+        const int64_t at = static_cast<int64_t>(r) * p.ldo + n0 + n;
+        if (p.out_bf16) static_cast<uint16_t*>(p.out)[at] = f32_to_bf16(v);
+        else static_cast<float*>(p.out)[at] = v;
+    }
+}
+
 // Tile plan of a grouped call: tile j covers tile_rows[j] positions of expert
 // tile_e[j]'s bucket from tile_p0[j].  Offsets are clamped to the call's pairs.
 __global__ void __launch_bounds__(1024) plan_i8_kernel(const int32_t* __restrict__ offsets, int E, int pairs,
@@ -511,6 +572,9 @@ PrefillWs prefill_ws(const moe355_layer_desc* d, int T) {
     return w;
 }
 
+// Which dense form: the tiles of 256 x 256 need some of them to pay.
+bool few_rows(int M, int N) { return M <= 64 || static_cast<int64_t>(M) * N <= FEW_OUTPUTS; }
+
 // One block per CU, a multiple of the XCDs; fewer where there are fewer tiles.
 unsigned grid_of(int64_t tiles) {
     static const int cus = [] {
@@ -575,6 +639,13 @@ extern "C" moe355_status moe355_matmul_i8(const int8_t* a, int64_t a_stride, con
     p.out_bf16 = out_type == MOE355_BF16;
     p.ldo = out_stride;
     p.paired = N % 2 == 0 && out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(out) % (p.out_bf16 ? 4 : 8) == 0;
+    if (few_rows(M, N)) {
+        const dim3 grid((N + 15) / 16, (M + 63) / 64);
+        if (M <= 16) few_rows_i8_kernel<1><<<grid, FEW_WAVES * WAVE, 0, stream>>>(p);
+        else if (M <= 32) few_rows_i8_kernel<2><<<grid, FEW_WAVES * WAVE, 0, stream>>>(p);
+        else few_rows_i8_kernel<4><<<grid, FEW_WAVES * WAVE, 0, stream>>>(p);
+        return check_launch("matmul_i8");
+    }
     gemm_i8_kernel<DENSE><<<grid_of(tiles), THREADS, 0, stream>>>(p);
     return check_launch("matmul_i8");
 }
