@@ -357,21 +357,28 @@ def combine(y, topk_w, out, stream=None):
 
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
+# These calls take a few microseconds on the GPU, and so should the way there: the
+# current stream's handle without a Stream object where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_one_gpu = None
+
 
 def _rows(t, dtype, name, shape=None):
     """Address and row stride (in elements) of a 2-D device tensor whose rows are contiguous."""
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be 2-D{'' if shape is None else f' of shape {shape}'}, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and t.shape[1] > 1:
         raise ValueError(f"{name}: the values of a row must be contiguous")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), ld
 
 
 def _flat(t, dtype, name, numel):
     """Address of a contiguous device tensor of exactly numel values."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != numel:
         raise ValueError(f"{name} must hold {numel} values, got {t.numel()}")
@@ -382,20 +389,27 @@ def _flat(t, dtype, name, numel):
 
 def _run(call, stream, tensors, *args):
     """The C call on the tensors' device: its current stream, or the given one."""
-    dev = tensors[0].device
+    global _one_gpu
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.device != dev or not t.is_cuda):
-            raise ValueError(f"{call}: every tensor must be on one GPU (got {t.device} and {dev})")
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError(f"{call}: every tensor must be on one GPU (got {t.device} and {tensors[0].device})")
     fn = getattr(load(), call)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device_index != dev.index:
-        raise ValueError(f"{call}: the stream belongs to GPU {s.device_index}, the tensors to {dev.index}")
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, s.cuda_stream)
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"{call}: the stream belongs to GPU {stream.device_index}, the tensors to {dev}")
+    else:
+        handle = stream.cuda_stream
+    if _one_gpu is None:
+        _one_gpu = torch.cuda.device_count() == 1
+    if _one_gpu or torch.cuda.current_device() == dev:
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, s.cuda_stream)
-    check(st, call)
+            st = fn(*args, handle)
+    if st != 0:
+        check(st, call)
 
 
 def route_scored(desc: RouterDesc, logits, bias, topk_ids, topk_w, stream=None):
