@@ -14,6 +14,8 @@
 // limit, are further apart than twice the fp32 error, or are equal in logit and bias
 // (an exact tie, lower id first).  About one token in a thousand fails that and is
 // decided in fp64.  Weights are fp64 in both.
+#include <type_traits>
+
 #include "internal.h"
 
 namespace moe355 {
@@ -354,6 +356,295 @@ __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_kernel(ScoreParams
     route_fp64<BF16, NPL>(p, t, choice_lds + static_cast<int64_t>(wv) * p.E);
 }
 
+// ---- up to 256 experts: four tokens per wavefront ---------------------------
+// A token has a row of 16 lanes, NE = 4, 8 or 16 experts a lane, and most
+// instructions serve four tokens.  The fp32 pass as above, on keys whose low bits
+// hold the entry's place in its lane: a lane sorts its keys once (a merge network of
+// minima and maxima), and a round takes the largest head of the row by four DPP
+// maxima over the upper bits, the lowest lane's among equals, and moves that lane on.
+// So entries with equal upper bits come in order of their ids.
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false));
+}
+template <int CTRL>
+__device__ __forceinline__ float dppf(float v) { return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v))); }
+// exchanges that meet every lane of a row of 16: neighbours, pairs, halves, ends
+constexpr int QP1 = 0xB1, QP2 = 0x4E, HALF_MIRROR = 0x141, MIRROR = 0x140, ROW_SHL1 = 0x101, ROW_ROR = 0x120;
+template <typename F>
+__device__ __forceinline__ uint32_t row_all_u32(uint32_t v, F f) {
+    v = f(v, dpp_u32<QP1>(v));
+    v = f(v, dpp_u32<QP2>(v));
+    v = f(v, dpp_u32<HALF_MIRROR>(v));
+    return f(v, dpp_u32<MIRROR>(v));
+}
+template <typename F>
+__device__ __forceinline__ float row_all_f32(float v, F f) {
+    v = f(v, dppf<QP1>(v));
+    v = f(v, dppf<QP2>(v));
+    v = f(v, dppf<HALF_MIRROR>(v));
+    return f(v, dppf<MIRROR>(v));
+}
+__device__ __forceinline__ double row_sum_f64(double v) {
+    auto step = [&](auto C) {
+        constexpr int CTRL = decltype(C)::value;
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint64_t o = static_cast<uint64_t>(dpp_u32<CTRL>(static_cast<uint32_t>(u >> 32))) << 32 | dpp_u32<CTRL>(static_cast<uint32_t>(u));
+        v += __builtin_bit_cast(double, o);
+    };
+    step(std::integral_constant<int, QP1>{});
+    step(std::integral_constant<int, QP2>{});
+    step(std::integral_constant<int, HALF_MIRROR>{});
+    step(std::integral_constant<int, MIRROR>{});
+    return v;
+}
+
+// e^x in fp64: x = n ln 2 + r, |r| <= 0.35, Taylor's series to r^13 (the next term is
+// below 5e-18); 0 and infinity beyond +-800.
+__device__ __forceinline__ double exp_f64(double x) {
+    x = fmin(fmax(x, -800.0), 800.0);
+    const double n = rint(x * 1.4426950408889634);
+    const double r = fma(n, -2.3190468138462996e-17, fma(n, -0.6931471805599453, x));   // ln 2 in two parts
+    double y = 1.0 / 6227020800.0;
+    y = fma(y, r, 1.0 / 479001600.0);
+    y = fma(y, r, 1.0 / 39916800.0);
+    y = fma(y, r, 1.0 / 3628800.0);
+    y = fma(y, r, 1.0 / 362880.0);
+    y = fma(y, r, 1.0 / 40320.0);
+    y = fma(y, r, 1.0 / 5040.0);
+    y = fma(y, r, 1.0 / 720.0);
+    y = fma(y, r, 1.0 / 120.0);
+    y = fma(y, r, 1.0 / 24.0);
+    y = fma(y, r, 1.0 / 6.0);
+    y = fma(y, r, 0.5);
+    y = fma(y, r, 1.0);
+    y = fma(y, r, 1.0);
+    return ldexp(y, static_cast<int>(n));
+}
+
+// The rank of this lane's group among the row's (LPG lanes each), and whether another
+// group has the same score.
+template <int LPG, int D = 1>
+__device__ __forceinline__ void group_rank(float g, int& rank, bool& same) {
+    if constexpr (D * LPG < 16) {
+        const float o = dppf<ROW_ROR + D * LPG>(g);
+        rank += o > g ? 1 : 0;
+        same = same || o == g;
+        group_rank<LPG, D + 1>(g, rank, same);
+    }
+}
+
+// D: results a row can give (k + 1 at most).  vec: quads of logits and biases are aligned.
+template <bool BF16, int NE, int D>
+__global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_rows_kernel(ScoreParams p, bool vec, int lpg) {
+    extern __shared__ double choice_lds[];
+    __shared__ int32_t sel[SR_WAVES][4][16];
+    const int wv = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1);
+    const int row = lane >> 4, j = lane & 15, e0 = j * NE;
+    const int t0 = (blockIdx.x * SR_WAVES + wv) * 4;
+    if (t0 >= p.T) return;   // whole wavefronts leave
+    const int E = p.E;
+    const bool soft = p.score == MOE355_SCORE_SOFTMAX;
+    const int64_t at = static_cast<int64_t>(min(t0 + row, p.T - 1)) * p.stride;
+
+    // All loads of a lane in flight together: places past the row's end read its last
+    // experts and are replaced.
+    float l[NE], b[NE];
+    if (vec) {   // E is a multiple of 4
+#pragma unroll
+        for (int q = 0; q < NE; q += 4) {
+            const int64_t from = at + min(e0 + q, E - 4);
+            if constexpr (BF16) {
+                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + from);
+                l[q] = __uint_as_float(v.x << 16);
+                l[q + 1] = __uint_as_float(v.x & 0xFFFF0000u);
+                l[q + 2] = __uint_as_float(v.y << 16);
+                l[q + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+            } else {
+                const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + from);
+                l[q] = v.x;
+                l[q + 1] = v.y;
+                l[q + 2] = v.z;
+                l[q + 3] = v.w;
+            }
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int q = 0; q < NE; q += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p.bias + min(e0 + q, E - 4));
+                b[q] = v.x;
+                b[q + 1] = v.y;
+                b[q + 2] = v.z;
+                b[q + 3] = v.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int64_t from = at + min(e0 + i, E - 1);
+            l[i] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p.logits)[from])
+                        : static_cast<const float*>(p.logits)[from];
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) b[i] = p.bias[min(e0 + i, E - 1)];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        l[i] = e0 + i < E ? l[i] : -3.0e38f;
+        b[i] = p.bias && e0 + i < E ? b[i] : 0.0f;
+    }
+    // infinities and NaN (also where a lane's product with 0 shows them), large biases
+    float odd = 0.0f, bmax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        odd = fmaf(l[i], 0.0f, odd);
+        odd = fmaf(b[i], 0.0f, odd);
+        bmax = fmaxf(bmax, __builtin_fabsf(b[i]));
+    }
+    bool fail = !(odd == 0.0f) || bmax >= 64.0f;
+
+    float s[NE], mx = 0.0f, es = 5e-7f, total = 1.0f;   // errors: see route_fp32
+    if (soft) {
+        mx = l[0];
+#pragma unroll
+        for (int i = 1; i < NE; ++i) mx = fmaxf(mx, l[i]);
+        mx = row_all_f32(mx, [](float x, float y) { return fmaxf(x, y); });
+        fail = fail || mx < -1.0e38f;   // the filler of short rows would count
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            s[i] = exp_fast(l[i] - mx);
+            total += s[i];
+        }
+        total = row_all_f32(total, [](float x, float y) { return x + y; });
+        const float r = 1.0f / total;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) s[i] *= r;
+        es = 1.5e-6f * r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[i]));
+    }
+    // keys: the choice without its last bits (1.9e-6 of it at NE = 16) and the place from the end
+    uint32_t key[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        key[i] = e0 + i < E ? (f32_order_key(s[i] + b[i]) & ~static_cast<uint32_t>(NE - 1)) | static_cast<uint32_t>(NE - 1 - i) : 0u;
+    auto value = [](uint32_t k) {
+        k &= ~static_cast<uint32_t>(NE - 1);
+        return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+    };
+
+    if (lpg) {
+        uint32_t a1 = key[0], a2 = 0u;
+#pragma unroll
+        for (int i = 1; i < NE; ++i) {
+            a2 = max(a2, min(a1, key[i]));
+            a1 = max(a1, key[i]);
+        }
+        auto merge = [&](uint32_t o1, uint32_t o2) {
+            a2 = max(min(a1, o1), max(a2, o2));
+            a1 = max(a1, o1);
+        };
+        if (lpg >= 2) merge(dpp_u32<QP1>(a1), dpp_u32<QP1>(a2));
+        if (lpg >= 4) merge(dpp_u32<QP2>(a1), dpp_u32<QP2>(a2));
+        if (lpg >= 8) merge(dpp_u32<HALF_MIRROR>(a1), dpp_u32<HALF_MIRROR>(a2));
+        const bool group = e0 < E;
+        const float g = group ? value(a1) + value(a2) : -2.0e38f;
+        int rank = 0;
+        bool same = false;
+        if (lpg == 1) group_rank<1>(g, rank, same);
+        else if (lpg == 2) group_rank<2>(g, rank, same);
+        else if (lpg == 4) group_rank<4>(g, rank, same);
+        else group_rank<8>(g, rank, same);
+        const bool kept = group && rank < p.topk_group;
+        const float low = row_all_f32(kept ? g : 3.0e38f, [](float x, float y) { return fminf(x, y); });
+        const float high = row_all_f32(group && !kept ? g : -3.0e38f, [](float x, float y) { return fmaxf(x, y); });
+        // Four scores' errors; with choices below m: the keys' lost bits, always towards
+        // minus infinity, 2 * 15 * 2^-23 m between two groups' sums, and the roundings of
+        // four choices (2^-24 m each) and two sums (2^-24 2 m each), 4.1e-6 m in all.
+        const float m = 1.0f + row_all_f32(bmax, [](float x, float y) { return fmaxf(x, y); });
+        fail = fail || (group && same) || !(low - high > 4.0f * es + 4.5e-6f * m);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) key[i] = kept ? key[i] : 0u;
+    }
+
+    // descending merge sort network (odd-even merges)
+#pragma unroll
+    for (int w = 1; w < NE; w *= 2)
+#pragma unroll
+        for (int d = w; d >= 1; d /= 2)
+#pragma unroll
+            for (int x = d % w; x + d < NE; x += 2 * d)
+#pragma unroll
+                for (int i = 0; i < d; ++i)
+                    if (x + i + d < NE && (x + i) / (2 * w) == (x + i + d) / (2 * w)) {
+                        const uint32_t hi = max(key[x + i], key[x + i + d]), lo = min(key[x + i], key[x + i + d]);
+                        key[x + i] = hi;
+                        key[x + i + d] = lo;
+                    }
+
+    const uint64_t rowbits = 0xFFFFull << (16 * row);
+    const uint64_t below = rowbits & ((1ull << lane) - 1);
+    uint32_t my_top = 0u;
+    for (int r = 0; r <= p.k; ++r) {
+        const uint32_t head = key[0] & ~static_cast<uint32_t>(NE - 1);
+        const uint32_t top = row_all_u32(head, [](uint32_t x, uint32_t y) { return max(x, y); });
+        const uint64_t holders = __ballot(head == top);
+        const bool own = head == top && top != 0u && (holders & below) == 0;
+        if (own) sel[wv][row][r] = e0 + NE - 1 - static_cast<int>(key[0] & (NE - 1));
+        my_top = j == r ? top : my_top;
+        constexpr int DEPTH = NE < D ? NE : D;
+        const uint32_t moved = own ? 0xFFFFFFFFu : 0u;   // one bit-field insert per place
+#pragma unroll
+        for (int q = 0; q + 1 < DEPTH; ++q) key[q] = (key[q] & ~moved) | (key[q + 1] & moved);
+        key[DEPTH - 1] &= ~moved;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wavefront's own LDS writes
+    const bool found = my_top != 0u && j <= p.k;
+    int e = found ? sel[wv][row][j] : E - 1;
+    const float le = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p.logits)[at + e])
+                          : static_cast<const float*>(p.logits)[at + e];
+    const float be = p.bias ? p.bias[e] : 0.0f, c = value(my_top);
+    // the next result of the row (lane j + 1; lane 15 has none and is never looked at: k <= 15)
+    const float nc = dppf<ROW_SHL1>(c), nl = dppf<ROW_SHL1>(le), nb = dppf<ROW_SHL1>(be);
+    const bool next = dpp_u32<ROW_SHL1>(found ? 1u : 0u) != 0u && j < p.k;
+    const bool tie = next && le == nl && be == nb;   // exactly equal choices, in order of their ids
+    const float near = 2.0f * es + 4.2e-6f * fmaxf(__builtin_fabsf(c), __builtin_fabsf(nc));
+    fail = fail || (next && !tie && !(c - nc > near)) || (j < p.k && !found);
+    // weights in fp64
+    const bool chosen = j < p.k;
+    double sc;
+    if (soft) {
+        sc = exp_f64(static_cast<double>(le) - static_cast<double>(mx));
+        if (p.renorm) {
+            const float mass = row_all_f32(chosen ? static_cast<float>(sc) : 0.0f, [](float x, float y) { return x + y; });
+            fail = fail || !(mass > 1e-6f);
+            sc /= static_cast<double>(total);
+        } else {
+            double z = 0.0;
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                if (e0 + i < E) z += exp_f64(static_cast<double>(l[i]) - static_cast<double>(mx));
+            sc /= row_sum_f64(z);
+        }
+    } else {
+        sc = 1.0 / (1.0 + exp_f64(-static_cast<double>(le)));
+    }
+    if (p.renorm) sc = sc / (row_sum_f64(chosen ? sc : 0.0) + 1e-20);
+    const uint64_t failed = __ballot(fail);
+    if (chosen && t0 + row < p.T && (failed & rowbits) == 0) {
+        p.ids[static_cast<int64_t>(t0 + row) * p.k + j] = e;
+        p.w[static_cast<int64_t>(t0 + row) * p.k + j] = static_cast<float>(sc * static_cast<double>(p.scale));
+    }
+    for (int r = 0; r < 4; ++r)
+        if ((failed >> (16 * r) & 0xFFFFull) && t0 + r < p.T)
+            route_fp64<BF16, NE / 4>(p, t0 + r, choice_lds + static_cast<int64_t>(wv) * E);
+}
+
 template <bool BF16>
 void launch_score_route(const ScoreParams& p, hipStream_t stream) {
     const unsigned blocks = (static_cast<unsigned>(p.T) + SR_WAVES - 1) / SR_WAVES;
@@ -368,6 +659,20 @@ void launch_score_route(const ScoreParams& p, hipStream_t stream) {
     const int width = BF16 ? 2 * NPL : NPL >= 4 ? 16 : 4 * NPL;   // alignment of a lane's load
     const bool vec = p.E % NPL == 0 && p.stride * (BF16 ? 2 : 4) % width == 0 &&
                      reinterpret_cast<uintptr_t>(p.logits) % width == 0;
+    // up to 256 experts and 15 choices: four tokens per wavefront, lane j of a row with
+    // experts [j NE, j NE + NE)
+    const int NE = p.E <= 64 ? 4 : p.E <= 128 ? 8 : 16, lpg_rows = limit ? gsize / NE : 0;
+    if (p.E <= 256 && p.k <= 15 && (!limit || (gsize % NE == 0 && (lpg_rows & (lpg_rows - 1)) == 0))) {
+        const bool quads = p.E % 4 == 0 && p.stride % 4 == 0 &&
+                           reinterpret_cast<uintptr_t>(p.logits) % (BF16 ? 8 : 16) == 0 &&
+                           reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
+        const unsigned groups = (static_cast<unsigned>(p.T) + 4 * SR_WAVES - 1) / (4 * SR_WAVES);
+        auto kr = NE == 4   ? score_route_rows_kernel<BF16, 4, 16>
+                  : NE == 8 ? (p.k <= 8 ? score_route_rows_kernel<BF16, 8, 9> : score_route_rows_kernel<BF16, 8, 16>)
+                            : (p.k <= 8 ? score_route_rows_kernel<BF16, 16, 9> : score_route_rows_kernel<BF16, 16, 16>);
+        kr<<<groups, SR_WAVES * WAVE, lds, stream>>>(p, quads, lpg_rows);
+        return;
+    }
     auto k = NPL == 1 ? score_route_kernel<BF16, 1>
              : NPL == 2 ? score_route_kernel<BF16, 2>
              : NPL == 4 ? score_route_kernel<BF16, 4>
