@@ -300,7 +300,8 @@ __device__ __forceinline__ bool route_fp32(const ScoreParams& p, int t, bool vec
         const float c = value(top);
         // two scores' errors, and the roundings of the two sums with a bias
         const float near = 2.0f * es + 2.4e-7f * fmaxf(__builtin_fabsf(last_c), __builtin_fabsf(c));
-        if (r > 0 && !(last_c - c > near) && !(lo == last_l && bo == last_b)) return false;
+        // the (k + 1)th has to be clear of the kth: behind a tie there may be a third, equal in fp32
+        if (r > 0 && !(last_c - c > near) && !(r < p.k && lo == last_l && bo == last_b)) return false;
         last_c = c;
         last_l = lo;
         last_b = bo;
@@ -356,13 +357,16 @@ __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_kernel(ScoreParams
     route_fp64<BF16, NPL>(p, t, choice_lds + static_cast<int64_t>(wv) * p.E);
 }
 
-// ---- up to 256 experts: four tokens per wavefront ---------------------------
+// ---- up to 256 experts and 14 choices: four tokens per wavefront ---------------------------
 // A token has a row of 16 lanes, NE = 4, 8 or 16 experts a lane, and most
 // instructions serve four tokens.  The fp32 pass as above, on keys whose low bits
 // hold the entry's place in its lane: a lane sorts its keys once (a merge network of
 // minima and maxima), and a round takes the largest head of the row by four DPP
 // maxima over the upper bits, the lowest lane's among equals, and moves that lane on.
-// So entries with equal upper bits come in order of their ids.
+// So entries with equal upper bits come in order of their ids.  The k + 2 best of these
+// keys are ranked by fp64 choices, and the next one bounds all that is left, equal logits
+// apart: few tokens are too close for that and are decided by route_fp64, whose 5 to 8 us
+// (one wavefront, from cold) show at the end of a launch.
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
@@ -435,7 +439,7 @@ __device__ __forceinline__ void group_rank(float g, int& rank, bool& same) {
     }
 }
 
-// D: results a row can give (k + 1 at most).  vec: quads of logits and biases are aligned.
+// D: places of a lane that can be looked at, k + 3 or all of its NE.  vec: quads of logits and biases are aligned.
 template <bool BF16, int NE, int D>
 __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_rows_kernel(ScoreParams p, bool vec, int lpg) {
     extern __shared__ double choice_lds[];
@@ -532,12 +536,15 @@ __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_rows_kernel(ScoreP
     uint32_t key[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i)
-        key[i] = e0 + i < E ? (f32_order_key(s[i] + b[i]) & ~static_cast<uint32_t>(NE - 1)) | static_cast<uint32_t>(NE - 1 - i) : 0u;
+        key[i] = (f32_order_key(e0 + i < E ? s[i] + b[i] : -3.0e38f) & ~static_cast<uint32_t>(NE - 1)) |
+                 static_cast<uint32_t>(NE - 1 - i);
+    constexpr uint32_t NONE = 0x02000000u;   // keys of the filler and 0 are below, those of choices above
     auto value = [](uint32_t k) {
         k &= ~static_cast<uint32_t>(NE - 1);
         return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
     };
 
+    bool in_kept = true;
     if (lpg) {
         uint32_t a1 = key[0], a2 = 0u;
 #pragma unroll
@@ -570,6 +577,7 @@ __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_rows_kernel(ScoreP
         fail = fail || (group && same) || !(low - high > 4.0f * es + 4.5e-6f * m);
 #pragma unroll
         for (int i = 0; i < NE; ++i) key[i] = kept ? key[i] : 0u;
+        in_kept = kept;
     }
 
     // descending merge sort network (odd-even merges)
@@ -590,38 +598,37 @@ __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_rows_kernel(ScoreP
     const uint64_t rowbits = 0xFFFFull << (16 * row);
     const uint64_t below = rowbits & ((1ull << lane) - 1);
     uint32_t my_top = 0u;
-    for (int r = 0; r <= p.k; ++r) {
+    for (int r = 0; r < p.k + 2; ++r) {
         const uint32_t head = key[0] & ~static_cast<uint32_t>(NE - 1);
         const uint32_t top = row_all_u32(head, [](uint32_t x, uint32_t y) { return max(x, y); });
         const uint64_t holders = __ballot(head == top);
-        const bool own = head == top && top != 0u && (holders & below) == 0;
+        const bool own = head == top && top >= NONE && (holders & below) == 0;
         if (own) sel[wv][row][r] = e0 + NE - 1 - static_cast<int>(key[0] & (NE - 1));
         my_top = j == r ? top : my_top;
-        constexpr int DEPTH = NE < D ? NE : D;
-        const uint32_t moved = own ? 0xFFFFFFFFu : 0u;   // one bit-field insert per place
+        const uint32_t moved = own ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-        for (int q = 0; q + 1 < DEPTH; ++q) key[q] = (key[q] & ~moved) | (key[q + 1] & moved);
-        key[DEPTH - 1] &= ~moved;
+        for (int q = 0; q + 1 < D; ++q) key[q] = (key[q] & ~moved) | (key[q + 1] & moved);
+        key[D - 1] &= ~moved;
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wavefront's own LDS writes
-    const bool found = my_top != 0u && j <= p.k;
-    int e = found ? sel[wv][row][j] : E - 1;
+    // Lanes 0 to k + 1: the candidates, from which fp64 takes k.  All that is left is below
+    // the largest head, give or take its error.
+    const bool cand = my_top >= NONE && j < p.k + 2;
+    const uint32_t left = row_all_u32(key[0], [](uint32_t x, uint32_t y) { return max(x, y); });
+    const int e = cand ? sel[wv][row][j] : E - 1;
     const float le = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p.logits)[at + e])
                           : static_cast<const float*>(p.logits)[at + e];
-    const float be = p.bias ? p.bias[e] : 0.0f, c = value(my_top);
-    // the next result of the row (lane j + 1; lane 15 has none and is never looked at: k <= 15)
-    const float nc = dppf<ROW_SHL1>(c), nl = dppf<ROW_SHL1>(le), nb = dppf<ROW_SHL1>(be);
-    const bool next = dpp_u32<ROW_SHL1>(found ? 1u : 0u) != 0u && j < p.k;
-    const bool tie = next && le == nl && be == nb;   // exactly equal choices, in order of their ids
-    const float near = 2.0f * es + 4.2e-6f * fmaxf(__builtin_fabsf(c), __builtin_fabsf(nc));
-    fail = fail || (next && !tie && !(c - nc > near)) || (j < p.k && !found);
-    // weights in fp64
-    const bool chosen = j < p.k;
+    const float be = p.bias ? p.bias[e] : 0.0f;
+    fail = fail || (j < p.k && !cand);
+
+    // scores in fp64
     double sc;
     if (soft) {
         sc = exp_f64(static_cast<double>(le) - static_cast<double>(mx));
-        if (p.renorm) {
-            const float mass = row_all_f32(chosen ? static_cast<float>(sc) : 0.0f, [](float x, float y) { return x + y; });
+        if (p.renorm && !p.bias) {
+            // the row's sum cancels but for the 1e-20 beside it, where fp32 does as long as the
+            // chosen hold some mass, and does not change the order
+            const float mass = row_all_f32(cand ? static_cast<float>(sc) : 0.0f, [](float x, float y) { return fmaxf(x, y); });
             fail = fail || !(mass > 1e-6f);
             sc /= static_cast<double>(total);
         } else {
@@ -634,11 +641,66 @@ __global__ void __launch_bounds__(SR_WAVES* WAVE) score_route_rows_kernel(ScoreP
     } else {
         sc = 1.0 / (1.0 + exp_f64(-static_cast<double>(le)));
     }
+
+    // The candidates' order: mostly that of the keys.  Two that are not equal in logit and
+    // bias have to be further apart than two evaluations in fp64 can differ.
+    const double choice = sc + static_cast<double>(be);
+    auto order = [&](double oc, float ol, float ob, int oe, bool there, bool& before) {
+        const bool equal = ol == le && ob == be;
+        const double apart = 1e-14 * (__builtin_fabs(oc) + __builtin_fabs(choice) + __builtin_fabsf(ob) + __builtin_fabsf(be));
+        before = there && (equal ? oe < e : oc > choice);
+        return !there || equal || __builtin_fabs(oc - choice) > apart;
+    };
+    int rank = j;
+    {
+        const uint64_t u = __builtin_bit_cast(uint64_t, choice);
+        const uint64_t o = static_cast<uint64_t>(dpp_u32<ROW_SHL1>(static_cast<uint32_t>(u >> 32))) << 32 |
+                           dpp_u32<ROW_SHL1>(static_cast<uint32_t>(u));
+        const bool there = dpp_u32<ROW_SHL1>(cand ? 1u : 0u) != 0u && cand;
+        bool swapped;
+        const bool clear = order(__builtin_bit_cast(double, o), dppf<ROW_SHL1>(le), dppf<ROW_SHL1>(be),
+                                 static_cast<int>(dpp_u32<ROW_SHL1>(static_cast<uint32_t>(e))), there, swapped);
+        fail = fail || !clear;
+        if (__ballot(swapped)) {
+            rank = 0;
+            for (int d = 1; d < 16; ++d) {
+                const int src = (lane & ~15) | ((j + d) & 15);
+                bool before;
+                const double oc = __shfl(choice, src, WAVE);
+                const float ol = __shfl(le, src, WAVE), ob = __shfl(be, src, WAVE);
+                const int oe = __shfl(e, src, WAVE), there2 = __shfl(cand ? 1 : 0, src, WAVE);
+                const bool apart = order(oc, ol, ob, oe, there2 && cand, before);
+                fail = fail || !apart;
+                rank += before ? 1 : 0;
+            }
+        }
+    }
+    const bool chosen = cand && rank < p.k;
+    const float rest = value(left);
+    // two scores' errors, the keys' lost bits (1.8e-6 of the value), roundings
+    const float near = 2.0f * es + 4.2e-6f * fmaxf(__builtin_fabsf(rest), __builtin_fabsf(static_cast<float>(choice)));
+    const uint64_t tight = __ballot(chosen && left >= NONE && !(static_cast<float>(choice) - rest > near));
+    if (tight) {
+        // Equal logits may run on behind the candidates (bf16 has few values); their ids are
+        // higher.  Everything else that could belong to the chosen has to be a candidate.
+        const uint64_t last = __ballot(chosen && rank == p.k - 1) & rowbits;
+        const int src = last ? __ffsll(static_cast<unsigned long long>(last)) - 1 : lane;
+        const float lk = __shfl(le, src, WAVE), bk = __shfl(be, src, WAVE);
+        const float ck = __shfl(static_cast<float>(choice), src, WAVE);
+        const float limit = ck - 2.0f * es - 4.4e-6f * __builtin_fabsf(ck);
+        int others = cand && value(my_top) > limit && !(le == lk && be == bk) ? -1 : 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            others += in_kept && e0 + i < E && value(f32_order_key(s[i] + b[i])) > limit && !(l[i] == lk && b[i] == bk) ? 1 : 0;
+        others = static_cast<int>(row_all_u32(static_cast<uint32_t>(others), [](uint32_t x, uint32_t y) { return x + y; }));
+        fail = fail || ((tight & rowbits) != 0 && others != 0);
+    }
+
     if (p.renorm) sc = sc / (row_sum_f64(chosen ? sc : 0.0) + 1e-20);
     const uint64_t failed = __ballot(fail);
     if (chosen && t0 + row < p.T && (failed & rowbits) == 0) {
-        p.ids[static_cast<int64_t>(t0 + row) * p.k + j] = e;
-        p.w[static_cast<int64_t>(t0 + row) * p.k + j] = static_cast<float>(sc * static_cast<double>(p.scale));
+        p.ids[static_cast<int64_t>(t0 + row) * p.k + rank] = e;
+        p.w[static_cast<int64_t>(t0 + row) * p.k + rank] = static_cast<float>(sc * static_cast<double>(p.scale));
     }
     for (int r = 0; r < 4; ++r)
         if ((failed >> (16 * r) & 0xFFFFull) && t0 + r < p.T)
@@ -659,17 +721,18 @@ void launch_score_route(const ScoreParams& p, hipStream_t stream) {
     const int width = BF16 ? 2 * NPL : NPL >= 4 ? 16 : 4 * NPL;   // alignment of a lane's load
     const bool vec = p.E % NPL == 0 && p.stride * (BF16 ? 2 : 4) % width == 0 &&
                      reinterpret_cast<uintptr_t>(p.logits) % width == 0;
-    // up to 256 experts and 15 choices: four tokens per wavefront, lane j of a row with
+    // up to 256 experts and 14 choices: four tokens per wavefront, lane j of a row with
     // experts [j NE, j NE + NE)
     const int NE = p.E <= 64 ? 4 : p.E <= 128 ? 8 : 16, lpg_rows = limit ? gsize / NE : 0;
-    if (p.E <= 256 && p.k <= 15 && (!limit || (gsize % NE == 0 && (lpg_rows & (lpg_rows - 1)) == 0))) {
+    if (p.E <= 256 && p.k <= 14 && (!limit || (gsize % NE == 0 && (lpg_rows & (lpg_rows - 1)) == 0))) {
         const bool quads = p.E % 4 == 0 && p.stride % 4 == 0 &&
                            reinterpret_cast<uintptr_t>(p.logits) % (BF16 ? 8 : 16) == 0 &&
                            reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
         const unsigned groups = (static_cast<unsigned>(p.T) + 4 * SR_WAVES - 1) / (4 * SR_WAVES);
-        auto kr = NE == 4   ? score_route_rows_kernel<BF16, 4, 16>
-                  : NE == 8 ? (p.k <= 8 ? score_route_rows_kernel<BF16, 8, 9> : score_route_rows_kernel<BF16, 8, 16>)
-                            : (p.k <= 8 ? score_route_rows_kernel<BF16, 16, 9> : score_route_rows_kernel<BF16, 16, 16>);
+        auto kr = NE == 4   ? score_route_rows_kernel<BF16, 4, 4>
+                  : NE == 8 ? score_route_rows_kernel<BF16, 8, 8>
+                  : p.k <= 8 ? score_route_rows_kernel<BF16, 16, 11>
+                             : score_route_rows_kernel<BF16, 16, 16>;
         kr<<<groups, SR_WAVES * WAVE, lds, stream>>>(p, quads, lpg_rows);
         return;
     }

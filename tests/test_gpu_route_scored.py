@@ -92,6 +92,40 @@ def test_choices_a_last_bit_apart(score):
     check(l, b, 16, score, 8, 3)
 
 
+@pytest.mark.parametrize("E", (40, 100, 256, 300))
+@pytest.mark.parametrize("k", (1, 3, 14, 15))
+def test_ties_that_hide_a_better_one(E, k):
+    """Scores equal in fp32 and not in fp64: k + 1 or more equal logits with low ids, one
+    that is larger by less than fp32's resolution of the score behind them."""
+    say("route_scored", "hidden", E, k)
+    logits = np.full((3, E), 16.0)
+    logits[0, E - 1] = 16.0625
+    logits[1, E // 2] = 16.0625
+    logits[1, E // 2 + 1] = 16.125
+    logits[2, : E // 2] = 0.0
+    logits[2, E - 2] = 16.0625
+    check(logits, None, k, "sigmoid")
+    check(logits, None, k, "sigmoid", dtype="bf16")
+
+
+@pytest.mark.parametrize("E,k,groups", [(60, 4, (1, 1)), (64, 14, (4, 2)), (100, 9, (1, 1)), (128, 8, (8, 2)),
+                                        (128, 5, (16, 5)), (200, 7, (1, 1)), (256, 8, (8, 4)), (256, 14, (2, 1)),
+                                        (256, 14, (16, 15)), (256, 9, (1, 1)), (160, 6, (5, 2))])
+@pytest.mark.parametrize("score", ("softmax", "sigmoid"))
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_many_tokens(E, k, groups, score, dtype):
+    """Close choices and ties in numbers: logits of few distinct values, exact and a little off."""
+    say("route_scored", "many", E, k, groups, score, dtype)
+    rng = np.random.default_rng(E * k)
+    logits = rng.normal(0, 1, (1500, E))
+    logits[500:1000] = np.round(logits[500:1000] * 8) / 8
+    logits[1000:] = np.round(logits[1000:] * 4) / 4 * (1 + rng.choice((0, 1e-7, 1e-6, 1e-5), (500, E)))
+    b = rng.normal(0, 0.1, E).astype(np.float32)
+    check(logits, b, k, score, groups[0], groups[1], dtype=dtype)
+    check(logits, None, k, score, groups[0], groups[1], renorm=False, dtype=dtype)
+    check(logits, np.round(b * 8) / 8, k, score, groups[0], groups[1], dtype=dtype)
+
+
 @pytest.mark.parametrize("score", ("softmax", "sigmoid"))
 @pytest.mark.parametrize("groups", ((1, 1), (8, 3)))
 @pytest.mark.parametrize("dtype", ("f32", "bf16"))
