@@ -6,19 +6,26 @@
 //            h = silu(g) u (moe355_expert_ffn_prefill_i8);
 //   down     the grouped product of h, one row of y per (token, slot) pair.
 //
-// Tile: 256 rows x 256 weight rows per block of eight wavefronts, two per SIMD; a
-// wavefront owns 128 rows and 64 weight rows (eight 32x32 accumulators).  The
-// activations are the first operand, so an accumulator holds rows (tokens) in its
+// Tile: 256 rows (short tiles: 64) x 256 weight rows per block of eight wavefronts, two
+// per SIMD; a wavefront owns half the rows and 64 weight rows (eight 32x32 accumulators,
+// or two).  The activations are the first operand, so an accumulator holds rows (tokens) in its
 // registers and a weight row per lane.
 //
 // K runs in stages of 128, whose rows are whole 128-byte lines: direct loads to
 // LDS of 128-byte row pieces reach 23.8 TB/s over the chip, of 64-byte pieces
-// 14.7 (one cache request each either way).  Two slots of 64 KB hold the stage in
-// use and the next.  Blocks are persistent (one per CU): the stages of a block's
+// 14.7 (one cache request each either way).  Two slots of 64 KB (three of 40 KB) hold
+// the stage in use and the next (two).  Blocks are persistent (one per CU): the stages of a block's
 // tiles form one stream, so the next tile's first two stages load under the
 // epilogue of the one before.
 //
-// What bounds it: power.  The same loop on registers and LDS alone sustains 2.9
+// Short tiles serve small products, where few blocks wait for their loads and the
+// matrix cores for both: a tile of K = 4096 takes 24 us against 51 of a tall one, one of
+// K = 512 takes 7.6 against 15.  Per row the tall ones read half as much, so they win
+// from three rounds of short tiles over the CUs on (3000 x 4096 x 4096: 67 us against
+// 82), and in the grouped products from about 96 pairs per expert on (64 experts of
+// 2048 x 768: 92 us short and 111 tall at 32 pairs, 128 and 141 at 96, 149 and 148 at 128).
+//
+// What bounds the tall ones: power.  The same loop on registers and LDS alone sustains 2.9
 // POP/s on random codes (4.9 on zeros).
 #include <type_traits>
 
@@ -28,12 +35,12 @@
 namespace moe355 {
 namespace {
 
-constexpr int BM = 256, BN = 256, BK = 128;
-constexpr int SLOT_A = BM * BK, SLOT = (BM + BN) * BK;   // bytes
+constexpr int BN = 256, BK = 128;
 constexpr int THREADS = 512;
 constexpr int NXCD = 8;
-constexpr int PIECES = SLOT / 2 / 1024 / (THREADS / WAVE);   // direct loads of each operand per wavefront and stage
-constexpr int GROUP_M = 4;   // dense: tiles run 4 rows of tiles at a time, weight columns outermost
+constexpr int TALL = 256, SHORT = 64;   // rows of a tile
+constexpr int TALL_COST = 2, SHORT_COST = 1;   // of a round of tiles: 51 us and 24 us at K = 4096
+constexpr int SHORT_PAIRS = 96;         // pairs per expert up to which a chunk takes them
 
 enum Kind { DENSE, GATE_UP, DOWN };
 
@@ -86,9 +93,15 @@ __device__ __forceinline__ void dma16_at(const void* base, uint32_t voff, uint32
                  :: "v"(voff), "s"(base), "s"(lds), "n"(AT) : "memory", "scc");
 }
 
-template <int KIND>
+template <int KIND, int BM>
 __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[2 * SLOT];
+    constexpr int SLOTS = BM == TALL ? 2 : 3;
+    constexpr int SLOT_A = BM * BK, SLOT = (BM + BN) * BK;   // bytes
+    // direct loads of each operand per wavefront and stage
+    constexpr int PA = SLOT_A / 1024 / (THREADS / WAVE), PB = BN * BK / 1024 / (THREADS / WAVE);
+    constexpr int MT_W = BM / 64;              // row tiles of 32 of a wavefront
+    constexpr int GROUP_M = 1024 / BM;         // dense: 1024 rows of tiles at a time, weight columns outermost
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[SLOTS * SLOT];
     __shared__ __attribute__((aligned(16))) float rscale[2][BM];   // scales of the rows of this tile and the next
     __shared__ __attribute__((aligned(16))) int64_t rrow[2][BM];   // down: byte offsets of their rows of y
     const int tid = threadIdx.x;
@@ -96,28 +109,29 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
     // The lane index is made opaque again for every tile, so that the compiler
     // recomputes what derives from it instead of keeping it in registers (they would
     // not suffice, and a spill's reload waits for every memory operation in flight).
-    int lane = tid & (WAVE - 1), ln = 0, hh = 0, lr = 0;   // lr: LDS row of load piece 0; piece j: + 8 j
+    int lane = tid & (WAVE - 1), ln = 0, hh = 0, la = 0, lb = 0;   // la, lb: LDS rows of load piece 0; piece j: + 8 j
     auto refresh_lane = [&]() {
         asm volatile("" : "+v"(lane));
         ln = lane & 31;
         hh = lane >> 5;
-        lr = 32 * wv + lane / 8;
+        la = 8 * PA * wv + lane / 8;
+        lb = 8 * PB * wv + lane / 8;
     };
     refresh_lane();
-    const int wm = wv >> 2, wn = wv & 3;   // the wavefront's 128 rows and 64 weight rows
+    const int wm = wv >> 2, wn = wv & 3;   // the wavefront's half of the rows and 64 weight rows
     const uint32_t ring_lds = lds_addr(ring);
 
     // Tiles of one XCD (block id mod 8) are consecutive: neighbours share an
     // expert's weights or activation rows in that XCD's L2.
     constexpr int PER_N = KIND == GATE_UP ? BN / 2 : BN;
     const int NT = (p.N + PER_N - 1) / PER_N;
-    const int MT = KIND == DENSE ? (p.M + BM - 1) / BM : ld_const(p.n_tiles);
+    const int MT = KIND == DENSE ? static_cast<int>((static_cast<int64_t>(p.M) + BM - 1) / BM) : ld_const(p.n_tiles);
     const int64_t total = static_cast<int64_t>(MT) * NT;
     const int xcd = blockIdx.x % NXCD, step_t = gridDim.x / NXCD;
     const int t_end = static_cast<int>(total * (xcd + 1) / NXCD);
     int t = static_cast<int>(total * xcd / NXCD) + blockIdx.x / NXCD;
     if (t >= t_end) return;
-    const int ks = max(2, (p.K + BK - 1) / BK);
+    const int ks = max(SLOTS, (p.K + BK - 1) / BK);
 
     auto tile_at = [&](int i) {
         Tile x;
@@ -146,9 +160,9 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
     // outputs), or for gate/up row f0 + 32 w + i of gate (ct = 0) and up (ct = 1).
     // Rows past the end repeat the last one.
     const void *abase, *bbase;
-    uint32_t aoff[PIECES], boff[PIECES];
+    uint32_t aoff[PA], boff[PB];
     bool a_rows = true;   // some of the wavefront's A rows exist (the others are not loaded, nor used)
-    auto set_source = [&](const Tile& x, const int (&tok)[PIECES]) {
+    auto set_source = [&](const Tile& x, const int (&tok)[PA]) {
         if (KIND == DENSE) {
             abase = uniform_ptr(p.a + static_cast<int64_t>(x.m0) * p.lda);
             bbase = uniform_ptr(p.b + static_cast<int64_t>(x.nt) * BN * p.ldb);
@@ -156,12 +170,16 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
             abase = uniform_ptr(KIND == GATE_UP ? p.a : p.a + static_cast<int64_t>(x.m0) * p.lda);
             bbase = uniform_ptr(blob_at(x) + p.q_off[0] + (KIND == DOWN ? static_cast<int64_t>(x.nt) * BN * p.ldb : 0));
         }
-        a_rows = 8 * PIECES * wv < x.rows;
+        a_rows = 8 * PA * wv < x.rows;
 #pragma unroll
-        for (int j = 0; j < PIECES; ++j) {
-            const int r = lr + 8 * j, c = ((lane & 7) ^ swz(r)) * 16;
+        for (int j = 0; j < PA; ++j) {
+            const int r = la + 8 * j;
             const int row = KIND == GATE_UP ? tok[j] : min(r, x.rows - 1);
-            aoff[j] = static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lda) + c;
+            aoff[j] = static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lda) + ((lane & 7) ^ swz(r)) * 16;
+        }
+#pragma unroll
+        for (int j = 0; j < PB; ++j) {
+            const int r = lb + 8 * j, c = ((lane & 7) ^ swz(r)) * 16;
             const int w = r >> 6, ct = (r >> 5) & 1, i = r & 31;
             if (KIND == GATE_UP) {
                 const int f = min(x.nt * (BN / 2) + 32 * w + i, p.N - 1);
@@ -177,29 +195,34 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
     // registers; the bases move.  (Four instructions a load: with the addresses and the
     // tail's test formed per load, the last load of a stage went out half a stage late.)
     auto load_full = [&](int kk, int slot) {
-        const uint32_t sl = ring_lds + slot * SLOT + PIECES * wv * 1024;
+        const uint32_t sa = ring_lds + slot * SLOT + PA * wv * 1024, sb = ring_lds + slot * SLOT + PB * wv * 1024;
         const int8_t *ab = static_cast<const int8_t*>(abase) + kk * BK, *bb = static_cast<const int8_t*>(bbase) + kk * BK;
-        dma16_at<SLOT_A>(bb, boff[0], sl);
-        dma16_at<SLOT_A + 1024>(bb, boff[1], sl);
-        dma16_at<SLOT_A + 2048>(bb, boff[2], sl);
-        dma16_at<SLOT_A + 3072>(bb, boff[3], sl);
+        dma16_at<SLOT_A>(bb, boff[0], sb);
+        dma16_at<SLOT_A + 1024>(bb, boff[1], sb);
+        dma16_at<SLOT_A + 2048>(bb, boff[2], sb);
+        dma16_at<SLOT_A + 3072>(bb, boff[3], sb);
         if (a_rows) {
-            dma16_at<0>(ab, aoff[0], sl);
-            dma16_at<1024>(ab, aoff[1], sl);
-            dma16_at<2048>(ab, aoff[2], sl);
-            dma16_at<3072>(ab, aoff[3], sl);
+            dma16_at<0>(ab, aoff[0], sa);
+            if constexpr (PA == 4) {
+                dma16_at<1024>(ab, aoff[1], sa);
+                dma16_at<2048>(ab, aoff[2], sa);
+                dma16_at<3072>(ab, aoff[3], sa);
+            }
         }
     };
     // A stage that ends past K: a chunk past it is fetched from the row's start instead
     // (in bounds; its A side is cleared before use).
     auto load_tail = [&](int kk, int slot) {
-        const uint32_t sl = ring_lds + slot * SLOT + PIECES * wv * 1024;
+        const uint32_t sa = ring_lds + slot * SLOT + PA * wv * 1024, sb = ring_lds + slot * SLOT + PB * wv * 1024;
 #pragma unroll
-        for (int j = 0; j < PIECES; ++j) {
-            const int c = ((lane & 7) ^ swz(lr + 8 * j)) * 16;
-            const uint32_t in = kk * BK + c < p.K ? kk * BK : static_cast<uint32_t>(-c);
-            dma16(abase, aoff[j] + in, sl + j * 1024);
-            dma16(bbase, boff[j] + in, sl + j * 1024 + SLOT_A);
+        for (int j = 0; j < PA; ++j) {
+            const int c = ((lane & 7) ^ swz(la + 8 * j)) * 16;
+            dma16(abase, aoff[j] + (kk * BK + c < p.K ? kk * BK : static_cast<uint32_t>(-c)), sa + j * 1024);
+        }
+#pragma unroll
+        for (int j = 0; j < PB; ++j) {
+            const int c = ((lane & 7) ^ swz(lb + 8 * j)) * 16;
+            dma16(bbase, boff[j] + (kk * BK + c < p.K ? kk * BK : static_cast<uint32_t>(-c)), sb + j * 1024 + SLOT_A);
         }
     };
     auto load_stage = [&](int kk, int slot) {
@@ -215,17 +238,17 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
         }
         __syncthreads();
     };
-    auto read_op = [&](int slot, int s, int i, Frag& f) {   // operand i (of 6) of step s
+    auto read_op = [&](int slot, int s, int i, Frag& f) {   // operand i (of 2 + MT_W) of step s
         const uint8_t* sp = ring + slot * SLOT;
         const int c = ((2 * s + hh) ^ swz(ln)) << 4;        // rows differ from ln by multiples of 32
         if (i < 2) f.b[i] = *reinterpret_cast<const i32x4*>(sp + SLOT_A + (64 * wn + 32 * i + ln) * BK + c);
-        else f.a[i - 2] = *reinterpret_cast<const i32x4*>(sp + (128 * wm + 32 * (i - 2) + ln) * BK + c);
+        else f.a[i - 2] = *reinterpret_cast<const i32x4*>(sp + (BM / 2 * wm + 32 * (i - 2) + ln) * BK + c);
     };
 
     // The scales (and rows of y) of a tile's rows, one row per thread, and the tokens
     // behind the LDS rows this lane loads of it.
     float my_scale = 0.0f;
-    int my_row = 0, tok[PIECES] = {};
+    int my_row = 0, tok[PA] = {};
     auto request_rows = [&](const Tile& x) {
         const int r = x.m0 + min(tid & (BM - 1), x.rows - 1);
         my_scale = p.as[KIND == GATE_UP ? p.row[r] : r];
@@ -240,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
     auto request_tokens = [&](const Tile& x) {
         if (KIND == GATE_UP) {
 #pragma unroll
-            for (int j = 0; j < PIECES; ++j) tok[j] = p.row[x.m0 + min(lr + 8 * j, x.rows - 1)];
+            for (int j = 0; j < PA; ++j) tok[j] = p.row[x.m0 + min(la + 8 * j, x.rows - 1)];
         }
     };
     auto next_of = [&](int i) { return i + step_t < t_end ? i + step_t : i; };   // at the end the tile itself
@@ -250,28 +273,29 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
     request_rows(cur);
     set_source(cur, tok);
     keep_rows(0);
-    load_stage(0, 0);
-    load_stage(1, 1);
-    int slot = 0, lk = 2;   // slot of the stage in use; next stage to load of the tile in aoff / boff
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) load_stage(i, i);
+    int slot = 0, lk = SLOTS;   // slot of the stage in use; next stage to load of the tile in aoff / boff
+    auto after = [&](int i) { return i + 1 < SLOTS ? i + 1 : 0; };   // the next slot
     Frag f[2];
-    stage_barrier<PIECES>();   // stage 0 has landed everywhere (stage 1 is at least so many loads)
+    stage_barrier<PB * (SLOTS - 1)>();   // stage 0 has landed everywhere (each later one is at least PB loads)
     if (p.K < BK) clear_tail(0, 0);
 #pragma unroll
-    for (int i = 0; i < 6; ++i) read_op(0, 0, i, f[0]);
-    bool stores_after = false;   // at least 32 stores were issued after the last loads
+    for (int i = 0; i < 2 + MT_W; ++i) read_op(0, 0, i, f[0]);
+    bool stores_after = false;   // at least 16 MT_W stores were issued after the last loads
     int par = 0;                 // this tile's half of rscale and rrow
 
     for (; t < t_end; t += step_t) {
         refresh_lane();
         request_rows(nxt);
         request_tokens(nxt);
-        i32x16 R[4][2];
+        i32x16 R[MT_W][2];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int mt = 0; mt < MT_W; ++mt)
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) R[mt][ct] = i32x16{};
         // Rows of the wavefront that exist: row tiles of 32 without any are skipped.
-        const int live = __builtin_amdgcn_readfirstlane(cur.rows - 128 * wm);
+        const int live = __builtin_amdgcn_readfirstlane(cur.rows - BM / 2 * wm);
         // The four K steps of a stage: while a step's MFMAs run, the next step's
         // operands are read from LDS into the other register set.  The stage's barrier
         // stands before its last step, whose operands are in registers by then: past it
@@ -291,16 +315,16 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
                     }
                     // the loads have landed; of a tile's first stage they are older than the
                     // stores of the epilogue before, which may still be on their way
-                    if (kk == 0 && stores_after) stage_barrier<32>();
-                    else stage_barrier<0>();
+                    if (kk == 0 && stores_after) stage_barrier<BM == TALL ? 32 : 16>();
+                    else stage_barrier<PB * (SLOTS - 2)>();
                     // the next stage ends past K: the last of this tile, or (K < 128) the first of the next
                     const int nk = kk + 1 < ks ? kk + 1 : 0;
-                    if ((nk + 1) * BK > p.K) clear_tail(nk, slot ^ 1);
+                    if ((nk + 1) * BK > p.K) clear_tail(nk, after(slot));
                     // what was requested about the next tile's rows has landed by now
                     if (kk == 1) keep_rows(par ^ 1);
                 }
 #pragma unroll
-                for (int mt = 0; mt < 4; ++mt) {
+                for (int mt = 0; mt < MT_W; ++mt) {
                     __builtin_amdgcn_sched_barrier(0);
                     if (32 * mt < live) {
 #pragma unroll
@@ -309,15 +333,15 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
                     }
                     if (s == 3 && mt == 0) load_stage(lk, slot);
 #pragma unroll
-                    for (int j = 2 * mt; j < 2 * mt + 2 && j < 6; ++j) {
+                    for (int j = 2 * mt; j < (mt + 1 < MT_W ? 2 * mt + 2 : 2 + MT_W); ++j) {
                         if (s < 3) read_op(slot, s + 1, j, f[(s + 1) & 1]);
-                        else read_op(slot ^ 1, 0, j, f[0]);
+                        else read_op(after(slot), 0, j, f[0]);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
             ++lk;
-            slot ^= 1;
+            slot = after(slot);
         }
 
         refresh_lane();
@@ -327,24 +351,24 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
         const int half = par;
         par ^= 1;
         // Element i of an accumulator is row 8 (i / 4) + 4 hh + i % 4 of its 32.
-        // 64 stores where every row is live and the wavefront's first output exists
-        stores_after = live >= 128 && now.nt * PER_N + (PER_N / 4) * wn < p.N;
+        // 16 MT_W stores where every row is live and the wavefront's first output exists
+        stores_after = live >= BM / 2 && now.nt * PER_N + (PER_N / 4) * wn < p.N;
         const float* bs0 = KIND == DENSE ? p.bs : reinterpret_cast<const float*>(blob_at(now) + p.s_off[0]);
-        const int r0 = 128 * wm + 4 * hh;
+        const int r0 = BM / 2 * wm + 4 * hh;
         // Loaded scales are waited for here: left to the rows' conditional blocks, every one
         // of them would wait for all of the stores before it.
         auto landed = [](float a, float b) { asm volatile("" ::"v"(a), "v"(b)); };
         auto each_row = [&](auto put) {   // put(mt, element, row past r0, its scale)
             auto rows = [&](auto ALLc) {
 #pragma unroll
-                for (int mt = 0; mt < 4; ++mt)
+                for (int mt = 0; mt < MT_W; ++mt)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int r = 32 * mt + 8 * (i >> 2) + (i & 3);
                         if (decltype(ALLc)::value || r0 + r < now.rows) put(mt, i, r, rscale[half][r0 + r]);
                     }
             };
-            if (live >= 128) rows(std::true_type{});
+            if (live >= BM / 2) rows(std::true_type{});
             else if (live > 0) rows(std::false_type{});
         };
         if (KIND == GATE_UP) {
@@ -398,29 +422,12 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the loads past the last tile have landed
 }
 
-// What each position of the buckets stands for: its token, and its row of y.  A
-// position whose pair is not one of the bucket's expert (ids out of range leave
-// such positions behind) computes token 0 into a row of y that nobody reads.
-__global__ void __launch_bounds__(256) rows_i8_kernel(const int32_t* __restrict__ perm,
-                                                      const int32_t* __restrict__ ids,
-                                                      const int32_t* __restrict__ offsets, int E, int k, int pairs,
-                                                      int32_t* __restrict__ tok, int32_t* __restrict__ yrow) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= pairs) return;
-    int pair = perm[i];
-    bool ok = pair >= 0 && pair < pairs;
-    const int e = ok ? ids[pair] : -1;
-    ok = e >= 0 && e < E && offsets[e] <= i && i < offsets[e + 1];
-    tok[i] = ok ? pair / k : 0;
-    yrow[i] = ok ? pair : pairs;
-}
-
 // Dense product of few rows: bound by reading the weights once and by latency, not by
 // the matrix cores.  A block owns 16 weight rows and up to 16 NT rows of A; its eight
 // wavefronts split K (v_mfma_i32_16x16x64_i8, the weights as the first operand) and
 // meet in LDS.
 constexpr int FEW_WAVES = 8;
-constexpr int64_t FEW_OUTPUTS = 1 << 20;
+constexpr int64_t FEW_OUTPUTS = 1 << 19;
 template <int NT>
 __global__ void __launch_bounds__(FEW_WAVES* WAVE) few_rows_i8_kernel(GemmParams p) {
     __shared__ i32x4 part[FEW_WAVES][NT][WAVE];
@@ -476,19 +483,49 @@ __global__ void __launch_bounds__(FEW_WAVES* WAVE) few_rows_i8_kernel(GemmParams
     }
 }
 
-// Tile plan of a grouped call: tile j covers tile_rows[j] positions of expert
-// tile_e[j]'s bucket from tile_p0[j].  Offsets are clamped to the call's pairs.
-__global__ void __launch_bounds__(1024) plan_i8_kernel(const int32_t* __restrict__ offsets, int E, int pairs,
-                                                       int max_tiles, int32_t* __restrict__ tile_e,
-                                                       int32_t* __restrict__ tile_p0,
-                                                       int32_t* __restrict__ tile_rows,
-                                                       int32_t* __restrict__ n_tiles) {
-    __shared__ int32_t wave_tot[16];
-    const int e = threadIdx.x, lane = e & (WAVE - 1), w = e / WAVE;
-    const int beg = e < E ? min(max(offsets[e], 0), pairs) : 0;
-    const int end = e < E ? min(max(offsets[e + 1], beg), pairs) : 0;
-    // tiles of about equal size, so that blocks that take the same number of tiles end together
-    const int nt = (end - beg + BM - 1) / BM;
+// What the products need beside the weights, in one launch: the tile list (block 0),
+// what each position of the buckets stands for, and x's codes and scales.
+//
+// Tiles are cut to about equal size per bucket, so that blocks that take the same
+// number of tiles end together.  A position's token, and its row of y: a position whose
+// pair is not one of the bucket's expert (ids out of range leave such positions behind)
+// computes token 0 into a row of y that nobody reads.  Quantisation: one wavefront per
+// row, as quantize_i8.
+constexpr int PREP = 1024;
+struct PrepParams {
+    const int32_t *offsets, *perm, *ids;
+    int E, k, pairs, bm, max_tiles, row_blocks;
+    int32_t *tile_e, *tile_p0, *tile_rows, *n_tiles, *tok, *yrow;
+    const uint16_t* x;
+    int T, H;
+    int8_t* xq;
+    float* xs;
+};
+__global__ void __launch_bounds__(PREP) prep_i8_kernel(PrepParams p) {
+    __shared__ int32_t wave_tot[PREP / WAVE];
+    const int lane = threadIdx.x & (WAVE - 1), w = threadIdx.x / WAVE;
+    if (static_cast<int>(blockIdx.x) > p.row_blocks) {
+        const int64_t t = static_cast<int64_t>(blockIdx.x - p.row_blocks - 1) * (PREP / WAVE) + w;
+        if (t >= p.T) return;
+        const float scale = quant_row(p.x + t * p.H, p.H, p.xq + t * p.H, lane);
+        if (lane == 0) p.xs[t] = scale;
+        return;
+    }
+    if (blockIdx.x > 0) {
+        const int64_t i = static_cast<int64_t>(blockIdx.x - 1) * PREP + threadIdx.x;
+        if (i >= p.pairs) return;
+        const int pair = p.perm[i];
+        bool ok = pair >= 0 && pair < p.pairs;
+        const int e = ok ? p.ids[pair] : -1;
+        ok = e >= 0 && e < p.E && p.offsets[e] <= i && i < p.offsets[e + 1];
+        p.tok[i] = ok ? pair / p.k : 0;
+        p.yrow[i] = ok ? pair : p.pairs;
+        return;
+    }
+    const int e = threadIdx.x;
+    const int beg = e < p.E ? min(max(p.offsets[e], 0), p.pairs) : 0;
+    const int end = e < p.E ? min(max(p.offsets[e + 1], beg), p.pairs) : 0;
+    const int nt = (end - beg + p.bm - 1) / p.bm;
     const int per = nt ? ((end - beg + nt - 1) / nt + 31) / 32 * 32 : 0;
     int inc = nt;
 #pragma unroll
@@ -499,17 +536,17 @@ __global__ void __launch_bounds__(1024) plan_i8_kernel(const int32_t* __restrict
     if (lane == WAVE - 1) wave_tot[w] = inc;
     __syncthreads();
     int base = 0, all = 0;
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < PREP / WAVE; ++i) {
         if (i < w) base += wave_tot[i];
         all += wave_tot[i];
     }
     base += inc - nt;
-    for (int i = 0; i < nt && base + i < max_tiles; ++i) {
-        tile_e[base + i] = e;
-        tile_p0[base + i] = beg + i * per;
-        tile_rows[base + i] = min(per, end - beg - i * per);
+    for (int i = 0; i < nt && base + i < p.max_tiles; ++i) {
+        p.tile_e[base + i] = e;
+        p.tile_p0[base + i] = beg + i * per;
+        p.tile_rows[base + i] = min(per, end - beg - i * per);
     }
-    if (e == 0) *n_tiles = min(all, max_tiles);
+    if (e == 0) *p.n_tiles = min(all, p.max_tiles);
 }
 
 // out[t] = sum over j ascending of w[t, j] y[t k + j] in fp32, rounded to bf16
@@ -544,7 +581,10 @@ __global__ void __launch_bounds__(256) combine_i8_kernel(const uint16_t* __restr
 
 int64_t align256(int64_t n) { return (n + 255) & ~int64_t{255}; }
 
-int max_tiles(int pairs, int E) { return pairs / BM + (pairs < E ? pairs : E); }
+// Rows of a tile of the grouped products.
+int tile_rows(int pairs, int E) { return pairs <= SHORT_PAIRS * E ? SHORT : TALL; }
+
+int max_tiles(int pairs, int E) { return pairs / tile_rows(pairs, E) + (pairs < E ? pairs : E); }
 
 // Regions of a prefill workspace.
 struct PrefillWs {
@@ -567,25 +607,36 @@ PrefillWs prefill_ws(const moe355_layer_desc* d, int T) {
     w.h = take(2 * tk * d->inter);
     w.hq = take(tk * d->inter);
     w.hs = take(4 * tk);
-    w.y = take(2 * (tk + 1) * d->hidden);   // one row more: see rows_i8_kernel
+    w.y = take(2 * (tk + 1) * d->hidden);   // one row more: see prep_i8_kernel
     w.bytes = at;
     return w;
 }
 
-// Which dense form: the tiles of 256 x 256 need some of them to pay.
+// Which dense form: up to 2^19 outputs, or 64 rows, no tiles (M = 256, N = 2048, K = 4096:
+// 20.8 us against 24.8 of the short tiles; M = 192, N = 4096: 29.6 against 25.2).
 bool few_rows(int M, int N) { return M <= 64 || static_cast<int64_t>(M) * N <= FEW_OUTPUTS; }
 
-// One block per CU, a multiple of the XCDs; fewer where there are fewer tiles.
-unsigned grid_of(int64_t tiles) {
-    static const int cus = [] {
-        int dev = 0, n = 0;
+// CUs, down to a multiple of the XCDs.
+int cus() {
+    static const int n = [] {
+        int dev = 0, c = 0;
         if (hipGetDevice(&dev) != hipSuccess ||
-            hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
-            n = 256;
-        return n < NXCD ? NXCD : n / NXCD * NXCD;
+            hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+            c = 256;
+        return c < NXCD ? NXCD : c / NXCD * NXCD;
     }();
+    return n;
+}
+
+// One block per CU; fewer where there are fewer tiles.
+unsigned grid_of(int64_t tiles) {
     const int64_t need = (tiles + NXCD - 1) / NXCD * NXCD;
-    return static_cast<unsigned>(need < cus ? need : cus);
+    return static_cast<unsigned>(need < cus() ? need : cus());
+}
+
+// Dense tiles: the tall ones if their rounds over the CUs cost no more.
+bool tall_tiles(int64_t tall, int64_t low) {
+    return (tall + cus() - 1) / cus() * TALL_COST < (low + cus() - 1) / cus() * SHORT_COST;
 }
 
 }  // namespace
@@ -623,7 +674,9 @@ extern "C" moe355_status moe355_matmul_i8(const int8_t* a, int64_t a_stride, con
     MOE355_REQUIRE(a_stride < (1ll << 23) && b_stride < (1ll << 23), MOE355_ENOTSUP,
                    "matmul_i8: row strides %lld, %lld of 2^23 bytes or more", static_cast<long long>(a_stride),
                    static_cast<long long>(b_stride));
-    const int64_t tiles = static_cast<int64_t>((M + BM - 1) / BM) * ((N + BN - 1) / BN);
+    const int64_t columns = (N + BN - 1) / BN;
+    const int64_t tall = (static_cast<int64_t>(M) + TALL - 1) / TALL * columns;
+    const int64_t tiles = (static_cast<int64_t>(M) + SHORT - 1) / SHORT * columns;
     MOE355_REQUIRE(tiles < (1ll << 31) - NXCD, MOE355_ENOTSUP, "matmul_i8: %lld tiles", static_cast<long long>(tiles));
     GemmParams p{};
     p.a = a;
@@ -646,7 +699,8 @@ extern "C" moe355_status moe355_matmul_i8(const int8_t* a, int64_t a_stride, con
         else few_rows_i8_kernel<4><<<grid, FEW_WAVES * WAVE, 0, stream>>>(p);
         return check_launch("matmul_i8");
     }
-    gemm_i8_kernel<DENSE><<<grid_of(tiles), THREADS, 0, stream>>>(p);
+    if (tall_tiles(tall, tiles)) gemm_i8_kernel<DENSE, TALL><<<grid_of(tall), THREADS, 0, stream>>>(p);
+    else gemm_i8_kernel<DENSE, SHORT><<<grid_of(tiles), THREADS, 0, stream>>>(p);
     return check_launch("matmul_i8");
 }
 
@@ -684,17 +738,31 @@ extern "C" moe355_status moe355_expert_ffn_prefill_i8(const moe355_layer_desc* d
     uint16_t* h = reinterpret_cast<uint16_t*>(base + w.h);
     uint16_t* y = reinterpret_cast<uint16_t*>(base + w.y);
 
-    plan_i8_kernel<<<1, 1024, 0, stream>>>(offsets, d->n_experts, pairs, mt, tiles, tiles + mt, tiles + 2 * mt,
-                                           tiles + 3 * mt);
-    st = check_launch("expert_ffn_prefill_i8 plan");
-    if (st) return st;
-    st = launch_quant_rows(x_bf16, H, T, H, xq, H, xs, stream, "expert_ffn_prefill_i8 quantise x");
-    if (st) return st;
     int32_t* tok = reinterpret_cast<int32_t*>(base + w.tok);
     int32_t* yrow = reinterpret_cast<int32_t*>(base + w.yrow);
-    rows_i8_kernel<<<(pairs + 255) / 256, 256, 0, stream>>>(perm, topk_ids, offsets, d->n_experts, d->top_k, pairs,
-                                                            tok, yrow);
-    st = check_launch("expert_ffn_prefill_i8 rows");
+    PrepParams r{};
+    r.offsets = offsets;
+    r.perm = perm;
+    r.ids = topk_ids;
+    r.E = d->n_experts;
+    r.k = d->top_k;
+    r.pairs = pairs;
+    r.bm = tile_rows(pairs, d->n_experts);
+    r.max_tiles = mt;
+    r.row_blocks = (pairs + PREP - 1) / PREP;
+    r.tile_e = tiles;
+    r.tile_p0 = tiles + mt;
+    r.tile_rows = tiles + 2 * mt;
+    r.n_tiles = tiles + 3 * mt;
+    r.tok = tok;
+    r.yrow = yrow;
+    r.x = static_cast<const uint16_t*>(x_bf16);
+    r.T = T;
+    r.H = H;
+    r.xq = xq;
+    r.xs = xs;
+    prep_i8_kernel<<<1 + r.row_blocks + (T + PREP / WAVE - 1) / (PREP / WAVE), PREP, 0, stream>>>(r);
+    st = check_launch("expert_ffn_prefill_i8 prepare");
     if (st) return st;
     GemmParams p{};
     p.S = L.bytes;
@@ -717,7 +785,9 @@ extern "C" moe355_status moe355_expert_ffn_prefill_i8(const moe355_layer_desc* d
         g.q_off[m] = L.q[m];
         g.s_off[m] = L.s[m];
     }
-    gemm_i8_kernel<GATE_UP><<<grid_of(static_cast<int64_t>(mt) * ((I + BN / 2 - 1) / (BN / 2))), THREADS, 0, stream>>>(g);
+    const bool tall = tile_rows(pairs, d->n_experts) == TALL;
+    (tall ? gemm_i8_kernel<GATE_UP, TALL> : gemm_i8_kernel<GATE_UP, SHORT>)
+        <<<grid_of(static_cast<int64_t>(mt) * ((I + BN / 2 - 1) / (BN / 2))), THREADS, 0, stream>>>(g);
     st = check_launch("expert_ffn_prefill_i8 gate_up");
     if (st) return st;
     st = launch_quant_rows(h, I, pairs, I, hq, I, hs, stream, "expert_ffn_prefill_i8 quantise h");
@@ -734,7 +804,8 @@ extern "C" moe355_status moe355_expert_ffn_prefill_i8(const moe355_layer_desc* d
     dn.ldo = H;
     dn.q_off[0] = dn.q_off[1] = L.q[2];
     dn.s_off[0] = dn.s_off[1] = L.s[2];
-    gemm_i8_kernel<DOWN><<<grid_of(static_cast<int64_t>(mt) * ((H + BN - 1) / BN)), THREADS, 0, stream>>>(dn);
+    (tall ? gemm_i8_kernel<DOWN, TALL> : gemm_i8_kernel<DOWN, SHORT>)
+        <<<grid_of(static_cast<int64_t>(mt) * ((H + BN - 1) / BN)), THREADS, 0, stream>>>(dn);
     st = check_launch("expert_ffn_prefill_i8 down");
     if (st) return st;
     const int64_t n8 = static_cast<int64_t>(T) * H / 8;

@@ -120,6 +120,81 @@ __global__ void __launch_bounds__(64) perm_scatter_kernel(const int32_t* __restr
     }
 }
 
+// Few pairs (a short chunk): the whole sort in one workgroup of 16 wavefronts, each
+// with a run of at most 256 consecutive pairs.  A pair's rank among the equal ids of
+// its run comes from ballots, the runs' counts per expert are summed in LDS.  One launch
+// of 4.4 us in place of three of 12.6 us at 999 pairs of 40 experts.
+constexpr int SMALL_PAIRS = 4096, SMALL_EXPERTS = 512, SMALL_WAVES = 16;
+__global__ void __launch_bounds__(SMALL_WAVES* WAVE) perm_small_kernel(const int32_t* __restrict__ ids, int n, int E,
+                                                                       int32_t* __restrict__ perm,
+                                                                       int32_t* __restrict__ offsets) {
+    extern __shared__ int32_t cnt[];   // [SMALL_WAVES][E]
+    __shared__ int32_t wave_tot[SMALL_WAVES];
+    const int lane = threadIdx.x & (WAVE - 1), w = threadIdx.x / WAVE;
+    constexpr int NG = SMALL_PAIRS / SMALL_WAVES / WAVE;
+    const int per = ((n + SMALL_WAVES - 1) / SMALL_WAVES + WAVE - 1) / WAVE * WAVE;   // at most NG * 64
+    const int beg = w * per, end = min(beg + per, n);
+    int idv[NG], rank[NG];
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+        const int i = beg + q * WAVE + lane;
+        idv[q] = q * WAVE < per && i < end ? ids[i] : -1;
+    }
+    for (int i = threadIdx.x; i < SMALL_WAVES * E; i += SMALL_WAVES * WAVE) cnt[i] = 0;
+    __syncthreads();
+    const int nbits = E > 1 ? 32 - __clz(E - 1) : 1;
+    const uint64_t below = (1ull << lane) - 1;
+    int32_t* mine = cnt + w * E;
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+        const int e = idv[q];
+        const bool valid = e >= 0 && e < E;
+        uint64_t peers = __ballot(valid);
+        for (int b = 0; b < nbits; ++b) {
+            const bool bit = valid && ((e >> b) & 1);
+            const uint64_t bal = __ballot(bit);
+            peers &= bit ? bal : ~bal;
+        }
+        rank[q] = -1;
+        int before = 0;
+        if (valid) before = mine[e];
+        __builtin_amdgcn_wave_barrier();
+        if (valid) {
+            rank[q] = before + __popcll(peers & below);
+            if ((peers & below) == 0) mine[e] = before + __popcll(peers);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    int total = 0;
+    if (e < E)
+        for (int i = 0; i < SMALL_WAVES; ++i) total += cnt[i * E + e];
+    int inc = total;
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) {
+        const int o = __shfl_up(inc, d, WAVE);
+        if (lane >= d) inc += o;
+    }
+    if (lane == WAVE - 1) wave_tot[w] = inc;
+    __syncthreads();
+    int acc = inc - total;
+    for (int i = 0; i < w; ++i) acc += wave_tot[i];
+    if (e < E) {
+        offsets[e] = acc;
+        for (int i = 0; i < SMALL_WAVES; ++i) {
+            const int c = cnt[i * E + e];
+            cnt[i * E + e] = acc;
+            acc += c;
+        }
+    }
+    if (e == 0) offsets[E] = n;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < NG; ++q)
+        if (rank[q] >= 0) perm[mine[idv[q]] + rank[q]] = beg + q * WAVE + lane;
+}
+
 }  // namespace
 
 size_t permute_ws_bytes(int E, int T, int k) {
@@ -131,6 +206,10 @@ size_t permute_ws_bytes(int E, int T, int k) {
 moe355_status launch_permute(const int32_t* ids, int n, int E, int32_t* perm, int32_t* offsets,
                              int32_t* hist, hipStream_t stream) {
     const int nb = (n + PCHUNK - 1) / PCHUNK;
+    if (n > 0 && n <= SMALL_PAIRS && E <= SMALL_EXPERTS) {
+        perm_small_kernel<<<1, SMALL_WAVES * WAVE, SMALL_WAVES * E * sizeof(int32_t), stream>>>(ids, n, E, perm, offsets);
+        return check_launch("permute");
+    }
     if (nb > 0) {
         perm_count_kernel<<<nb, 256, E * sizeof(int32_t), stream>>>(ids, n, E, hist);
         moe355_status st = check_launch("permute count");

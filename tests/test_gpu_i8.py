@@ -113,6 +113,15 @@ def test_matmul_against_64_bits(M, N, K, out_type):
         assert np.all(np.abs(got - want) <= tol), np.abs(got - want).max()
 
 
+@pytest.mark.parametrize("M,N,K", [(520, 1025, 16), (641, 900, 48), (1024, 513, 128), (700, 1001, 400),
+                                   (1025, 514, 272), (130, 9000, 1040), (2049, 4101, 16), (2300, 3500, 80),
+                                   (2600, 3301, 400), (70000, 48, 144), (2700, 4097, 512)])
+@pytest.mark.parametrize("out_type", ("f32", "bf16"))
+def test_matmul_tiles_against_64_bits(M, N, K, out_type):
+    """Sizes of the tiled forms: several tiles per block, ragged ones, K below and beside a stage."""
+    test_matmul_against_64_bits(M, N, K, out_type)
+
+
 def test_matmul_extremes():
     """The largest sums int32 has to hold, zero scales, and a row whose scale is NaN."""
     K = 65536
@@ -217,7 +226,41 @@ def test_prefill_against_64_bits(T, H, I, E, k):
     assert (L.prefill(x, ids, w) == out).all()                # the same on every run
 
 
-@pytest.mark.parametrize("T,k", ((300, 1), (260, 2)))
+@pytest.mark.parametrize("T,H,I,E,k", [(1000, 192, 128, 6, 2), (700, 64, 64, 4, 1), (1200, 320, 448, 3, 2),
+                                       (97, 128, 64, 1, 1), (2000, 128, 576, 16, 1), (513, 1024, 704, 2, 2)])
+def test_prefill_long_buckets_against_64_bits(T, H, I, E, k):
+    """More than 96 pairs per expert: the tall tiles, one or several a bucket."""
+    test_prefill_against_64_bits(T, H, I, E, k)
+
+
+@pytest.mark.parametrize("n,E", [(1, 1), (63, 7), (64, 512), (1023, 3), (4095, 512), (4096, 130), (4096, 513), (4097, 512)])
+def test_permute_short(n, E):
+    """The sort of few pairs in one workgroup beside the one of many; ids out of range
+    stand in no bucket."""
+    import torch
+    import moe_expert_layer_02_amd as m
+    say("permute", n, E)
+    rng = np.random.default_rng(n + E)
+    ids = rng.integers(0, E, n).astype(np.int32)
+    d = m.LayerDesc(64, 64, E, 1, m.ROUTE_SOFTMAX_TOPK, 1, 1, 1.0, m.W_INT8)
+    for bad in (False, True):
+        if bad:
+            ids[rng.random(n) < 0.2] = -1
+            ids[n // 2] = E
+        t = torch.from_numpy(ids).cuda().view(n, 1)
+        perm = torch.full((n,), -5, dtype=torch.int32, device="cuda")
+        off = torch.full((E + 2,), -5, dtype=torch.int32, device="cuda")
+        ws = torch.empty(max(1, m.workspace_bytes(d, n, m.MODE_PERMUTE)), dtype=torch.uint8, device="cuda")
+        m.permute(d, t, perm, off[:E + 1], ws)
+        valid = (ids >= 0) & (ids < E)
+        order = np.argsort(np.where(valid, ids, E), kind="stable")[:valid.sum()]
+        starts = np.concatenate([[0], np.cumsum(np.bincount(ids[valid], minlength=E))])
+        starts[E] = n
+        assert (off.cpu().numpy() == np.append(starts, -5)).all()
+        assert (perm.cpu().numpy() == np.append(order, np.full(n - len(order), -5))).all()
+
+
+@pytest.mark.parametrize("T,k", ((300, 1), (260, 2), (900, 1), (1100, 2)))
 def test_prefill_one_expert_takes_all(T, k):
     """One bucket of several tiles beside empty ones; the same expert twice in a token."""
     L = Layer(192, 128, 6, k, T)
