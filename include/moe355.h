@@ -124,7 +124,7 @@ typedef struct {
 int64_t moe355_expert_bytes(const moe355_layer_desc* d);
 
 /*
- * The device layout, read by every expert FFN call and kept in the pool, the
+ * The device layout, read by every FFN call of the 4-bit formats and kept in the pool, the
  * cache slots and the prefill layer buffer: the same regions at the same
  * offsets, each cut into blocks of 16 output rows x 128 inputs, block
  * (rt, kc) at index rt * (in/128) + kc.

@@ -584,7 +584,9 @@ int64_t align256(int64_t n) { return (n + 255) & ~int64_t{255}; }
 // Rows of a tile of the grouped products.
 int tile_rows(int pairs, int E) { return pairs <= SHORT_PAIRS * E ? SHORT : TALL; }
 
-int max_tiles(int pairs, int E) { return pairs / tile_rows(pairs, E) + (pairs < E ? pairs : E); }
+// Room for the tile list: the short tiles' bound for either, so that a workspace for a
+// long chunk also holds a shorter one's list.
+int max_tiles(int pairs, int E) { return pairs / SHORT + (pairs < E ? pairs : E); }
 
 // Regions of a prefill workspace.
 struct PrefillWs {

@@ -42,6 +42,16 @@ def test_sizes(abi):
             assert L.moe355_workspace_bytes(ctypes.byref(q), 4, abi.MODE_PREFILL_I8) == 0
 
 
+@pytest.mark.parametrize("H,I,E,k", ((64, 64, 1024, 1), (64, 64, 40, 3), (256, 128, 16, 2), (1344, 704, 40, 8)))
+def test_a_workspace_for_a_long_chunk_holds_a_shorter_one(abi, H, I, E, k):
+    """Sizes grow with T, also where a chunk changes to another tile."""
+    L, d = abi.load(), i8_desc(abi, H, I, E, k)
+    for mode, last in ((abi.MODE_PREFILL_I8, 120 * E // k + 2), (abi.MODE_DECODE_I8, 256 // k), (abi.MODE_PERMUTE, 5000)):
+        step = 1 if last < 20000 else 7
+        sizes = [L.moe355_workspace_bytes(ctypes.byref(d), T, mode) for T in range(0, last, step)]
+        assert all(x <= y for x, y in zip(sizes, sizes[1:])), mode
+
+
 def test_four_bit_calls_refuse_int8_experts(abi):
     L, d = abi.load(), i8_desc(abi)
     r = ctypes.byref(d)
