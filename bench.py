@@ -30,7 +30,8 @@ HBM_PEAK_GBS = 8000.0
 # sources of the decode FFN kernels (a recorded traffic figure is void once they change)
 DECODE_SOURCES = ["moe_expert_layer_02_amd/csrc/decode.hip", "moe_expert_layer_02_amd/csrc/internal.h",
                   "moe_expert_layer_02_amd/csrc/classify_dev.h", "moe_expert_layer_02_amd/csrc/route_dev.h"]
-PREFILL_SOURCES = ["moe_expert_layer_02_amd/csrc/prefill.hip", "moe_expert_layer_02_amd/csrc/internal.h"]
+PREFILL_SOURCES = ["moe_expert_layer_02_amd/csrc/prefill.hip", "moe_expert_layer_02_amd/csrc/internal.h",
+                   "moe_expert_layer_02_amd/csrc/lds_dma.h"]
 METRIC = "decode MoE-layer expert-weight GB/s (% HBM peak); prefill tokens/s (% MFMA peak)"
 
 
