@@ -358,15 +358,25 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
         // Loaded scales are waited for here: left to the rows' conditional blocks, every one
         // of them would wait for all of the stores before it.
         auto landed = [](float a, float b) { asm volatile("" ::"v"(a), "v"(b)); };
-        auto each_row = [&](auto put) {   // put(mt, element, row past r0, its scale)
+        // Scales and row offsets are read for four rows at a time and outside the rows'
+        // conditions (behind each one, a partial tile spent an LDS trip per row).
+        auto each_row = [&](auto put) {   // put(mt, element, row past r0, its scale, its offset in y)
             auto rows = [&](auto ALLc) {
 #pragma unroll
-                for (int mt = 0; mt < MT_W; ++mt)
+                for (int mt = 0; mt < MT_W; ++mt) {
+                    if (!decltype(ALLc)::value && 32 * mt >= live) continue;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = 32 * mt + 8 * (i >> 2) + (i & 3);
-                        if (decltype(ALLc)::value || r0 + r < now.rows) put(mt, i, r, rscale[half][r0 + r]);
+                    for (int g = 0; g < 4; ++g) {
+                        const int r = 32 * mt + 8 * g;
+                        float rs[4];
+                        int64_t ro[4] = {};
+                        __builtin_memcpy(rs, __builtin_assume_aligned(&rscale[half][r0 + r], 16), 16);
+                        if (KIND == DOWN) __builtin_memcpy(ro, __builtin_assume_aligned(&rrow[half][r0 + r], 16), 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (decltype(ALLc)::value || r0 + r + i < now.rows) put(mt, 4 * g + i, r + i, rs[i], ro[i]);
                     }
+                }
             };
             if (live >= BM / 2) rows(std::true_type{});
             else if (live > 0) rows(std::false_type{});
@@ -378,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
                 const float gs = bs0[fe], us = bs1[fe];
                 landed(gs, us);
                 uint16_t* h = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(now.m0 + r0) * p.ldo + fe;
-                each_row([&](int mt, int i, int r, float xs) {
+                each_row([&](int mt, int i, int r, float xs, int64_t) {
                     h[static_cast<int64_t>(r) * p.ldo] = swiglu_bf16(R[mt][0][i], R[mt][1][i], xs, gs, us);
                 });
             }
@@ -388,13 +398,13 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
                 const bool two = n + 1 < p.N;
                 const float s0 = bs0[n], s1 = bs0[two ? n + 1 : n];
                 landed(s0, s1);
-                each_row([&](int mt, int i, int r, float rs) {
+                each_row([&](int mt, int i, int r, float rs, int64_t ro) {
                     const float v0 = static_cast<float>(R[mt][0][i]) * rs * s0;
                     const float v1 = static_cast<float>(R[mt][1][i]) * rs * s1;
                     if (KIND == DOWN) {
                         // y in bf16: one more rounding of 2^-9 per expert output, for half the
                         // traffic of the [pairs, H] intermediate
-                        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + rrow[half][r0 + r] + 2 * n) = pack_bf16(v0, v1);
+                        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + ro + 2 * n) = pack_bf16(v0, v1);
                         return;
                     }
                     const int64_t o = static_cast<int64_t>(now.m0 + r0 + r) * p.ldo + n;
