@@ -36,9 +36,14 @@ def _pool_ptr(t) -> int:
     return t.data_ptr()
 
 
+# Calls of a few microseconds on the GPU, and so should the way there be: the current
+# stream's handle without a Stream object where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream)
 
 
 def _need(t, dtype, name):
@@ -357,10 +362,6 @@ def combine(y, topk_w, out, stream=None):
 
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
-# These calls take a few microseconds on the GPU, and so should the way there: the
-# current stream's handle without a Stream object where torch offers it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _one_gpu = None
 
 
