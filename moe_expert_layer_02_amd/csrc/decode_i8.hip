@@ -5,7 +5,9 @@
 // v_mfma_i32_16x16x64_i8 with the weights as the first operand (16 rows x 64
 // inputs) and up to 16 pairs of the expert as the second, so one pass over an
 // expert's bytes serves its pairs; bound by the weight bytes of the distinct
-// experts, and by the chain of launches and loads where those are few.
+// experts (16 tokens of 6 experts, H 4096, I 2048: 355 us, 5.7 TB/s of expert bytes), and
+// by the chain of launches and loads where those are few (one token of 8 experts, H 2048,
+// I 512: 12.5 us for 25 MB).
 //
 // Two kernels: gate/up (h in bf16 by pair) and down with the combine.  A down block
 // owns 16 output rows of every token: the pairs' results meet in LDS and are summed
@@ -42,13 +44,18 @@ struct DecodeI8 {
     const float* hs;
     uint16_t* out;
     const uint16_t* x;
+    int early;                  // weights are requested before the pairs are known
     int lds_rows;               // bytes of one quantised row in LDS (0: rows are quantised already)
 };
 
 // A small call: rows quantised by every block.  Gate/up: one row per wavefront of its
-// four; down: at most this many values of h.
-constexpr int INLINE_TOKENS = 4, INLINE_H = 8192, INLINE_VALUES = 16384;
-constexpr int EARLY_PAIRS = 16;
+// four (H = 2048, I = 512, 8 experts a token: one token 12.5 us against 13.9 with a launch
+// before it, four 30.7 against 32.0; INLINE_H bounds the rows' LDS); down: at most this
+// many values of h (4096: 12.5 us against 13.4; 8192 even; 16384: 27.5 against 25.5).
+constexpr int INLINE_TOKENS = 4, INLINE_H = 8192, INLINE_VALUES = 12288;
+// Calls of so few pairs and gate/up blocks (two per CU) request weights first: 256 blocks
+// 12.5 us against 13.1, 512 20.3 against 20.9; 768 (H = 4096, I = 2048) 39.4 against 36.1.
+constexpr int EARLY_PAIRS = 16, EARLY_BLOCKS = 512;
 
 // Where an expert's bytes are: its cache slot, or the pool.
 __device__ __forceinline__ const uint8_t* blob_of(const DecodeI8& p, int e, int slot) {
@@ -114,7 +121,7 @@ __global__ void __launch_bounds__(256) gate_up_i8_kernel(DecodeI8 p) {
     // In a call of few pairs the weights are requested before anything else is known
     // about the expert's pairs; in a larger one many pairs share an expert, and the first
     // of them has to be found before (loading first read 1.2 times the bytes at 96 pairs).
-    const bool early = p.uniq || p.pairs <= EARLY_PAIRS;
+    const bool early = p.uniq || p.early;
     auto find_pairs = [&]() {
         __syncthreads();
         if (wv == 0) {
@@ -415,7 +422,8 @@ extern "C" moe355_status moe355_expert_ffn_decode_i8(const moe355_layer_desc* d,
     }
     const int items = exp ? (pairs < p.E ? pairs : p.E) : pairs;
     p.lds_rows = inline_x ? p.H + 16 : 0;
-    auto gate_up = pairs <= EARLY_PAIRS ? gate_up_i8_kernel<8> : gate_up_i8_kernel<4>;
+    p.early = pairs <= EARLY_PAIRS && p.I / 16 * items <= EARLY_BLOCKS;
+    auto gate_up = p.early ? gate_up_i8_kernel<8> : gate_up_i8_kernel<4>;
     gate_up<<<dim3(p.I / 16, items), 256, static_cast<size_t>(p.lds_rows) * T, stream>>>(p);
     st = check_launch("expert_ffn_decode_i8 gate_up");
     if (st) return st;

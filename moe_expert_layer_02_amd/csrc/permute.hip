@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(64) perm_scatter_kernel(const int32_t* __restr
 // Few pairs (a short chunk): the whole sort in one workgroup of 16 wavefronts, each
 // with a run of at most 256 consecutive pairs.  A pair's rank among the equal ids of
 // its run comes from ballots, the runs' counts per expert are summed in LDS.  One launch
-// of 4.4 us in place of three of 12.6 us at 999 pairs of 40 experts.
+// of 4.6 us in place of three of 12.6 us at 999 pairs of 40 experts.
 constexpr int SMALL_PAIRS = 4096, SMALL_EXPERTS = 512, SMALL_WAVES = 16;
 __global__ void __launch_bounds__(SMALL_WAVES* WAVE) perm_small_kernel(const int32_t* __restrict__ ids, int n, int E,
                                                                        int32_t* __restrict__ perm,
