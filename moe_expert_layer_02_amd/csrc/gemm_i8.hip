@@ -201,14 +201,14 @@ __global__ void __launch_bounds__(THREADS, 2) gemm_i8_kernel(GemmParams p) {
         const int8_t *ab = static_cast<const int8_t*>(abase) + kk * BK, *bb = static_cast<const int8_t*>(bbase) + kk * BK;
         dma16_at<SLOT_A>(bb, boff[0], sb);
         dma16_at<SLOT_A + 1024>(bb, boff[1], sb);
-        dma16_at<SLOT_A + 2048>(bb, boff[2], sb);
-        dma16_at<SLOT_A + 3072>(bb, boff[3], sb);
+        dma16_at<SLOT_A + 2 * 1024>(bb, boff[2], sb);
+        dma16_at<SLOT_A + 3 * 1024>(bb, boff[3], sb);
         if (a_rows) {
             dma16_at<0>(ab, aoff[0], sa);
             if constexpr (PA == 4) {
                 dma16_at<1024>(ab, aoff[1], sa);
-                dma16_at<2048>(ab, aoff[2], sa);
-                dma16_at<3072>(ab, aoff[3], sa);
+                dma16_at<2 * 1024>(ab, aoff[2], sa);
+                dma16_at<3 * 1024>(ab, aoff[3], sa);
             }
         }
     };
